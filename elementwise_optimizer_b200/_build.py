@@ -35,11 +35,13 @@ MARSHAL_SRC = os.path.join(PKG, "csrc", "opt2s_marshal.cpp")
 MARSHAL_DIR = os.path.join(PKG, "_build")
 MARSHAL_NAME = "opt2s_marshal"
 
-COMMON = ["opt2s_kernel.cu", "opt2s_kernel8.cu", "opt2s_noalloc.cu", "opt2s_api8.cpp", "opt2s_ipc.cpp"]
+COMMON = ["opt2s_kernel.cu", "opt2s_kernel8.cu", "opt2s_noalloc.cu", "opt2s_api8.cpp", "opt2s_ipc.cpp",
+          "opt2s_mx4_quant.cu", "opt2s_mx4_gemm.cu", "opt2s_mx4_api.cpp"]
 API = "opt2s_api.cpp"
 TESTING_ONLY = ["opt2s_testing.cu"]
 SOURCES = [os.path.join(CSRC, f) for f in COMMON + [API] + TESTING_ONLY]
 HEADERS = [os.path.join(CSRC, "opt2s_internal.h"), os.path.join(CSRC, "opt2s_device.cuh"),
+           os.path.join(CSRC, "opt2s_mx4.cuh"),
            os.path.join(INCLUDE, "opt2s.h"), os.path.join(INCLUDE, "opt2s_testing.h")]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

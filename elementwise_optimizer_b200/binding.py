@@ -89,6 +89,19 @@ class TensorListDesc8(ctypes.Structure):
     _fields_ = [("tensors", ctypes.POINTER(opt2s_tensor8)), ("count", ctypes.c_int32)]
 
 
+class opt2s_mx4(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("slabs", ctypes.c_int64),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
+
+
+class opt2s_mx4_source(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("noise", ctypes.c_void_p), ("slabs", ctypes.c_int64),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("row_stride", ctypes.c_int64),
+                ("slab_stride", ctypes.c_int64), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+MX4_BLOCK = 32
+MX4_MAX_GROUPS = 1024
 BLOCK8 = 2048
 MIN_8BIT_SIZE = 4096
 
@@ -137,6 +150,24 @@ EXPORTS = {
     "opt2s_ipc_open": (ctypes.c_int, [ctypes.POINTER(opt2s_ipc_handle), ctypes.c_int64,
                                       ctypes.POINTER(ctypes.c_void_p), ctypes.POINTER(ctypes.c_void_p)]),
     "opt2s_ipc_close": (ctypes.c_int, [ctypes.c_void_p]),
+    "opt2s_mx4_code_bytes": (ctypes.c_int64, [ctypes.c_int64] * 3),
+    "opt2s_mx4_scale_bytes": (ctypes.c_int64, [ctypes.c_int64] * 3),
+    "opt2s_mx4_quantize": (ctypes.c_int, [ctypes.POINTER(opt2s_mx4_source), ctypes.POINTER(opt2s_mx4),
+                                          ctypes.POINTER(opt2s_mx4), ctypes.c_void_p, ctypes.c_int32,
+                                          ctypes.c_void_p]),
+    "opt2s_mx4_dequantize": (ctypes.c_int, [ctypes.POINTER(opt2s_mx4), ctypes.c_void_p, ctypes.c_int32,
+                                            ctypes.c_void_p]),
+    "opt2s_mx4_matmul": (ctypes.c_int, [ctypes.POINTER(opt2s_mx4), ctypes.POINTER(opt2s_mx4), ctypes.c_void_p,
+                                        ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p]),
+    "opt2s_mx4_matmul_grouped": (ctypes.c_int, [ctypes.POINTER(opt2s_mx4), ctypes.POINTER(opt2s_mx4),
+                                                ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                                ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
+                                                ctypes.c_int32, ctypes.c_void_p]),
+    "opt2s_mx4_matmul_ragged": (ctypes.c_int, [ctypes.POINTER(opt2s_mx4), ctypes.POINTER(opt2s_mx4),
+                                               ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                               ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
+                                               ctypes.c_void_p]),
+    "opt2s_mx4_errors": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32)]),
     "opt2s_release_cache": (ctypes.c_int, []),
     "opt2s_error_string": (ctypes.c_char_p, [ctypes.c_int]),
     "opt2s_last_cuda_error": (ctypes.c_int, []),

@@ -357,4 +357,59 @@ int record_cuda_error(cudaError_t e);
 // opt2s_api.cpp.
 void count_launches(int64_t n);
 
+// ---------------------------------------------------------------------------
+// Microscaled 4-bit matrices (opt2s_mx4_*.cu).  Layouts as in opt2s.h.
+// ---------------------------------------------------------------------------
+struct Mx4QuantArgs {
+    const void* x;
+    const uint8_t* noise;             // null: nearest
+    int64_t slabs, rows, cols;
+    int64_t row_stride, slab_stride;  // of x, in elements
+    uint8_t* codes;                   // blocks along the rows, or null
+    uint8_t* scales;
+    uint8_t* codes_t;                 // blocks down the columns, transposed, or null
+    uint8_t* scales_t;
+    const int32_t* offsets;           // ragged groups of rows, or null
+    int32_t groups;
+    int32_t vec, noise_vec;           // 16-byte accesses are aligned
+};
+// row_tiles: 128-row tiles a slab has (with groups: the column form's columns / 128).
+cudaError_t launch_mx4_quantize(const Mx4QuantArgs& a, int dtype, int64_t row_tiles, cudaStream_t stream);
+
+struct Mx4DequantArgs {
+    const uint8_t* codes;
+    const uint8_t* scales;
+    void* out;
+    int64_t slabs, rows, cols;
+    int32_t vec;
+};
+cudaError_t launch_mx4_dequantize(const Mx4DequantArgs& a, int dtype, cudaStream_t stream);
+
+// A product's operand: code rows of `pitch` bytes (a multiple of 64) and
+// scale words by 128-column group.
+struct Mx4Operand {
+    const uint8_t* codes;
+    const uint8_t* scales;
+    int64_t code_rows, pitch, scale_rows;
+};
+struct Mx4GemmOperands {
+    Mx4Operand x, w;      // token side and weight side (ragged contraction: rows and columns of D)
+};
+struct Mx4GemmArgs {
+    void* d;
+    int64_t ldd;
+    const int32_t* offsets;     // groups of token rows, or null
+    int64_t x_rows;             // token rows (ragged contraction: tokens)
+    int64_t w_rows, w_sf_rows;  // weight rows a slab has, and scale rows
+    int64_t p_rows;             // ragged contraction: rows of each D
+    int64_t d_cols;
+    int32_t groups;
+    int32_t k64;                // 64-element steps of the contraction
+    int32_t ragged_k;           // the groups cut the contraction
+    int32_t accumulate, fill_rest, dtype, vec;
+    int32_t split, tiles, w_tiles, p_tiles, q_tiles;    // set by the launch
+};
+cudaError_t launch_mx4_gemm(Mx4GemmArgs a, const Mx4GemmOperands& op, cudaStream_t stream);
+cudaError_t mx4_error_count(unsigned int* out);
+
 }  // namespace opt2s

@@ -1,0 +1,222 @@
+// opt2s_mx4_api.cpp -- the C ABI of the microscaled 4-bit operators
+// (include/opt2s.h): argument validation and launches.  Nothing here keeps
+// state: a call's tables travel as kernel arguments.
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "opt2s.h"
+#include "opt2s_internal.h"
+
+#define OPT2S_API extern "C" __attribute__((visibility("default")))
+
+using opt2s::Range;
+
+namespace {
+
+constexpr int64_t kMaxIndex = int64_t{1} << 30;     // rows and columns that tile indices may reach
+
+int64_t up(int64_t x, int64_t k) { return (x + k - 1) / k * k; }
+
+bool good_dtype(int32_t d) { return d == OPT2S_F32 || d == OPT2S_F16 || d == OPT2S_BF16; }
+
+bool good_sizes(int64_t slabs, int64_t rows, int64_t cols)
+{
+    if (slabs < 1 || rows < 0 || cols < 1 || slabs > kMaxIndex || rows > kMaxIndex || cols > kMaxIndex) return false;
+    return slabs * up(rows, 4) <= kMaxIndex;
+}
+
+Range span(const void* p, int64_t bytes, bool written)
+{
+    const auto lo = reinterpret_cast<uintptr_t>(p);
+    return {lo, lo + static_cast<uintptr_t>(bytes), written};
+}
+
+bool aligned(const void* p, uintptr_t k) { return reinterpret_cast<uintptr_t>(p) % k == 0; }
+
+// Checks a matrix and appends its two ranges (none when it has no rows).
+int matrix_ranges(const opt2s_mx4* m, bool written, Range* out, size_t* n)
+{
+    if (!m || !good_sizes(m->slabs, m->rows, m->cols)) return OPT2S_ERR_INVALID_ARG;
+    if (m->rows == 0) return OPT2S_OK;
+    if (!m->codes || !m->scales || !aligned(m->codes, 16) || !aligned(m->scales, 16)) return OPT2S_ERR_INVALID_ARG;
+    out[(*n)++] = span(m->codes, opt2s_mx4_code_bytes(m->slabs, m->rows, m->cols), written);
+    out[(*n)++] = span(m->scales, opt2s_mx4_scale_bytes(m->slabs, m->rows, m->cols), written);
+    return OPT2S_OK;
+}
+
+int good_groups(const int32_t* offsets, int32_t groups)
+{
+    if (!offsets || groups < 1 || groups > OPT2S_MX4_MAX_GROUPS || !aligned(offsets, 4)) return OPT2S_ERR_INVALID_ARG;
+    return OPT2S_OK;
+}
+
+opt2s::Mx4Operand operand(const opt2s_mx4* m)
+{
+    return {m->codes, m->scales, m->slabs * m->rows, up(m->cols, 128) / 2, m->slabs * up(m->rows, 4)};
+}
+
+// What the three products have in common.  d_rows rows of d_cols columns.
+int product(const opt2s_mx4* a, const opt2s_mx4* b, const int32_t* offsets, int32_t groups, bool ragged, void* d,
+            int64_t d_rows, int64_t ldd, int32_t dtype, int32_t accumulate, int32_t fill_rest, cudaStream_t stream)
+{
+    Range r[6];
+    size_t n = 0;
+    int st = matrix_ranges(a, false, r, &n);
+    if (st == OPT2S_OK) st = matrix_ranges(b, false, r, &n);
+    if (st != OPT2S_OK) return st;
+    if (!good_dtype(dtype) || (accumulate != 0 && accumulate != 1) || (fill_rest != 0 && fill_rest != 1))
+        return OPT2S_ERR_INVALID_ARG;
+    if (a->cols != b->cols || a->slabs != 1 || (accumulate && fill_rest)) return OPT2S_ERR_INVALID_ARG;
+    if (ldd < b->rows || ldd > (int64_t{1} << 40)) return OPT2S_ERR_INVALID_ARG;
+    if (d_rows == 0 || b->rows == 0) return OPT2S_OK;
+    const int es = opt2s::elem_bytes(dtype);
+    if (!d || !aligned(d, es)) return OPT2S_ERR_INVALID_ARG;
+    r[n++] = span(d, ((d_rows - 1) * ldd + b->rows) * es, true);
+    if (offsets) r[n++] = span(offsets, (static_cast<int64_t>(groups) + 1) * 4, false);
+    if ((st = opt2s::overlap_status(r, n)) != OPT2S_OK) return st;
+    opt2s::Mx4GemmArgs g{};
+    g.d = d;
+    g.ldd = ldd;
+    g.offsets = offsets;
+    g.groups = groups;
+    g.x_rows = ragged ? a->cols - 128 * static_cast<int64_t>(groups) : a->rows;
+    g.w_rows = b->rows;
+    g.w_sf_rows = up(b->rows, 4);
+    g.p_rows = a->rows;
+    g.d_cols = b->rows;
+    g.k64 = static_cast<int32_t>((a->cols + 63) / 64);
+    g.ragged_k = ragged;
+    g.accumulate = accumulate;
+    g.fill_rest = fill_rest;
+    g.dtype = dtype;
+    g.vec = aligned(d, 16) && ldd * es % 16 == 0;
+    const cudaError_t e = opt2s::launch_mx4_gemm(g, {operand(a), operand(b)}, stream);
+    if (e == cudaErrorInvalidConfiguration) return OPT2S_ERR_TOO_LARGE;
+    if (e != cudaSuccess) return opt2s::record_cuda_error(e);
+    opt2s::count_launches(1);
+    return OPT2S_OK;
+}
+
+}  // namespace
+
+OPT2S_API int64_t opt2s_mx4_code_bytes(int64_t slabs, int64_t rows, int64_t cols)
+{
+    return good_sizes(slabs, rows, cols) ? slabs * rows * (up(cols, 128) / 2) : -1;
+}
+
+OPT2S_API int64_t opt2s_mx4_scale_bytes(int64_t slabs, int64_t rows, int64_t cols)
+{
+    return good_sizes(slabs, rows, cols) ? up(cols, 128) / 128 * slabs * up(rows, 4) * 4 : -1;
+}
+
+OPT2S_API int opt2s_mx4_quantize(const opt2s_mx4_source* src, const opt2s_mx4* q, const opt2s_mx4* qt,
+                                 const int32_t* offsets, int32_t groups, cudaStream_t stream)
+{
+    OPT2S_RANGE("opt2s_mx4_quantize");
+    if (!src || src->reserved != 0 || !good_dtype(src->dtype)) return OPT2S_ERR_INVALID_ARG;
+    if (!good_sizes(src->slabs, src->rows, src->cols) || src->row_stride < 0 || src->slab_stride < 0)
+        return OPT2S_ERR_INVALID_ARG;
+    if (src->row_stride > (int64_t{1} << 40) || src->slab_stride > (int64_t{1} << 40)) return OPT2S_ERR_INVALID_ARG;
+    if (!offsets && groups != 0) return OPT2S_ERR_INVALID_ARG;
+    if (offsets && (good_groups(offsets, groups) != OPT2S_OK || src->slabs != 1)) return OPT2S_ERR_INVALID_ARG;
+    Range r[7];
+    size_t n = 0;
+    int st = OPT2S_OK;
+    if (q) {
+        if (q->slabs != src->slabs || q->rows != src->rows || q->cols != src->cols) return OPT2S_ERR_INVALID_ARG;
+        if ((st = matrix_ranges(q, true, r, &n)) != OPT2S_OK) return st;
+    }
+    const int64_t t_cols = offsets ? up(src->rows, 128) + 128 * static_cast<int64_t>(groups) : src->rows;
+    if (qt) {
+        if (qt->slabs != src->slabs || qt->rows != src->cols || qt->cols != t_cols) return OPT2S_ERR_INVALID_ARG;
+        if ((st = matrix_ranges(qt, true, r, &n)) != OPT2S_OK) return st;
+    }
+    const int64_t row_tiles = up(t_cols, 128) / 128;
+    if (row_tiles > 65535 || src->slabs > 65535) return OPT2S_ERR_TOO_LARGE;
+    if (row_tiles == 0 || (!q && !qt)) return OPT2S_OK;
+    if (src->rows > 0) {
+        const int es = opt2s::elem_bytes(src->dtype);
+        if (!src->x || !aligned(src->x, es)) return OPT2S_ERR_INVALID_ARG;
+        r[n++] = span(src->x, ((src->slabs - 1) * src->slab_stride + (src->rows - 1) * src->row_stride + src->cols) * es,
+                      false);
+        if (src->noise) r[n++] = span(src->noise, src->slabs * src->rows * src->cols, false);
+    }
+    if (offsets) r[n++] = span(offsets, (static_cast<int64_t>(groups) + 1) * 4, false);
+    if ((st = opt2s::overlap_status(r, n)) != OPT2S_OK) return st;
+    opt2s::Mx4QuantArgs a{};
+    const int es = opt2s::elem_bytes(src->dtype);
+    a.x = src->x;
+    a.noise = src->noise;
+    a.slabs = src->slabs;
+    a.rows = src->rows;
+    a.cols = src->cols;
+    a.row_stride = src->row_stride;
+    a.slab_stride = src->slab_stride;
+    if (q) { a.codes = q->codes; a.scales = q->scales; }
+    if (qt) { a.codes_t = qt->codes; a.scales_t = qt->scales; }
+    a.offsets = offsets;
+    a.groups = groups;
+    a.vec = aligned(src->x, 16) && src->row_stride * es % 16 == 0 && src->slab_stride * es % 16 == 0;
+    a.noise_vec = aligned(src->noise, 16) && src->cols % 16 == 0;
+    const cudaError_t e = opt2s::launch_mx4_quantize(a, src->dtype, row_tiles, stream);
+    if (e != cudaSuccess) return opt2s::record_cuda_error(e);
+    opt2s::count_launches(1);
+    return OPT2S_OK;
+}
+
+OPT2S_API int opt2s_mx4_dequantize(const opt2s_mx4* q, void* out, int32_t dtype, cudaStream_t stream)
+{
+    OPT2S_RANGE("opt2s_mx4_dequantize");
+    Range r[3];
+    size_t n = 0;
+    int st = matrix_ranges(q, false, r, &n);
+    if (st != OPT2S_OK) return st;
+    if (!good_dtype(dtype)) return OPT2S_ERR_INVALID_ARG;
+    if (q->rows == 0) return OPT2S_OK;
+    const int es = opt2s::elem_bytes(dtype);
+    if (!out || !aligned(out, es)) return OPT2S_ERR_INVALID_ARG;
+    r[n++] = span(out, q->slabs * q->rows * q->cols * es, true);
+    if ((st = opt2s::overlap_status(r, n)) != OPT2S_OK) return st;
+    const opt2s::Mx4DequantArgs a{q->codes, q->scales, out, q->slabs, q->rows, q->cols,
+                                  aligned(out, 16) && q->cols % 8 == 0};
+    const cudaError_t e = opt2s::launch_mx4_dequantize(a, dtype, stream);
+    if (e != cudaSuccess) return opt2s::record_cuda_error(e);
+    opt2s::count_launches(1);
+    return OPT2S_OK;
+}
+
+OPT2S_API int opt2s_mx4_matmul(const opt2s_mx4* a, const opt2s_mx4* b, void* d, int64_t ldd, int32_t dtype,
+                               int32_t accumulate, cudaStream_t stream)
+{
+    OPT2S_RANGE("opt2s_mx4_matmul");
+    if (!a || !b || b->slabs != 1) return OPT2S_ERR_INVALID_ARG;
+    return product(a, b, nullptr, 0, false, d, a->rows, ldd, dtype, accumulate, 0, stream);
+}
+
+OPT2S_API int opt2s_mx4_matmul_grouped(const opt2s_mx4* a, const opt2s_mx4* b, const int32_t* offsets,
+                                       int32_t groups, void* d, int64_t ldd, int32_t dtype, int32_t accumulate,
+                                       int32_t fill_rest, cudaStream_t stream)
+{
+    OPT2S_RANGE("opt2s_mx4_matmul_grouped");
+    if (!a || !b || good_groups(offsets, groups) != OPT2S_OK || b->slabs != groups) return OPT2S_ERR_INVALID_ARG;
+    return product(a, b, offsets, groups, false, d, a->rows, ldd, dtype, accumulate, fill_rest, stream);
+}
+
+OPT2S_API int opt2s_mx4_matmul_ragged(const opt2s_mx4* a, const opt2s_mx4* b, const int32_t* offsets,
+                                      int32_t groups, void* d, int64_t ldd, int32_t dtype, int32_t accumulate,
+                                      cudaStream_t stream)
+{
+    OPT2S_RANGE("opt2s_mx4_matmul_ragged");
+    if (!a || !b || good_groups(offsets, groups) != OPT2S_OK || b->slabs != 1) return OPT2S_ERR_INVALID_ARG;
+    if (a->cols < 128 * static_cast<int64_t>(groups) || a->cols % 128 != 0) return OPT2S_ERR_INVALID_ARG;
+    if (groups * a->rows > kMaxIndex) return OPT2S_ERR_TOO_LARGE;
+    return product(a, b, offsets, groups, true, d, groups * a->rows, ldd, dtype, accumulate, 0, stream);
+}
+
+OPT2S_API int opt2s_mx4_errors(uint32_t* count)
+{
+    if (!count) return OPT2S_ERR_INVALID_ARG;
+    const cudaError_t e = opt2s::mx4_error_count(count);
+    return e == cudaSuccess ? OPT2S_OK : opt2s::record_cuda_error(e);
+}

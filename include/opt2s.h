@@ -412,6 +412,115 @@ int opt2s_step_8bit(const TensorListDesc8 *desc, const Hyper *hyper, int step,
  * means OPT2S_MIN_8BIT_SIZE). */
 int opt2s_8bit_state_bits(int64_t numel, int64_t min_8bit_size);
 
+/*
+ * Microscaled 4-bit matrices: the weights a step updates, held in 4 bits for
+ * the products that read them, and those products.
+ *
+ * The format is MXFP4 of the OCP Microscaling Formats (MX) specification
+ * v1.0.  A row is cut into blocks of OPT2S_MX4_BLOCK = 32 elements; a block
+ * shares the scale 2^e, e = max(floor(log2(amax)) - 2, -127), kept as the byte
+ * e + 127 (E8M0), and each element is the E2M1 value (0, 0.5, 1, 1.5, 2, 3,
+ * 4, 6 and their negatives: codes 0-7, +8 for the sign) nearest to x / 2^e,
+ * ties to the even code, magnitudes above 6 taken as 6.  A block that holds
+ * an infinity or a NaN gets the scale byte 255 (NaN: the whole block reads as
+ * NaN) and codes 0.  Element types narrower than fp32 are widened exactly.
+ *
+ * Stochastic rounding takes its random numbers as an input, one byte r per
+ * element: where x / 2^e (saturated) lies a fraction f of the way from one
+ * code's magnitude to the next, the upper is taken when f > (r + 0.5) / 256.
+ *
+ * opt2s_mx4 is `slabs` matrices of rows x cols, blocks along cols:
+ *   codes   [slabs * rows][cols_p / 2] bytes, cols_p = cols rounded up to 128;
+ *           two elements a byte, the lower index in the low nibble; codes 0
+ *           behind cols
+ *   scales  [cols_p / 128][slabs * rows_p][4] bytes, rows_p = rows rounded up
+ *           to 4: the four blocks of a row in one 128-column group together,
+ *           so that any range of rows is contiguous
+ * Both pointers are DEVICE memory owned by the caller, 16-byte aligned.
+ * cols >= 1; rows may be 0.  The calls below keep nothing between calls,
+ * allocate nothing and may be captured in a CUDA graph.
+ */
+#define OPT2S_MX4_BLOCK 32
+#define OPT2S_MX4_MAX_GROUPS 1024
+
+typedef struct {
+    uint8_t *codes;
+    uint8_t *scales;
+    int64_t slabs, rows, cols;
+} opt2s_mx4;
+
+/* Bytes of codes and of scales of such a matrix (-1: invalid sizes). */
+int64_t opt2s_mx4_code_bytes(int64_t slabs, int64_t rows, int64_t cols);
+int64_t opt2s_mx4_scale_bytes(int64_t slabs, int64_t rows, int64_t cols);
+
+/* The source of a quantisation: slabs of rows x cols elements (OPT2S_F32,
+ * OPT2S_F16 or OPT2S_BF16), element (s, r, c) at x[s * slab_stride +
+ * r * row_stride + c] (strides >= 0).  noise: null for nearest, or
+ * slabs * rows * cols random bytes in that order (contiguous). */
+typedef struct {
+    const void *x;
+    const uint8_t *noise;
+    int64_t slabs, rows, cols;
+    int64_t row_stride, slab_stride;
+    int32_t dtype;
+    int32_t reserved;               /* must be 0 */
+} opt2s_mx4_source;
+
+/*
+ * Quantises `src` in one launch into q (blocks along the rows: slabs, rows,
+ * cols as the source) and/or qt (blocks down the columns, transposed: slabs,
+ * rows = the source's cols, cols = its rows); either may be null.  Both forms
+ * come from one read of the source, and use the same noise byte for an
+ * element.
+ *
+ * offsets (DEVICE, groups + 1 int32, non-decreasing; groups <=
+ * OPT2S_MX4_MAX_GROUPS; null for none) cuts the rows of a source of one slab
+ * into groups [offsets[e], offsets[e+1]).  q then holds the rows that lie in a
+ * group (others are left as they were).  In qt each group starts at a
+ * multiple of 128 columns (the sum of the earlier groups' sizes, each rounded
+ * up to 128), and qt->cols must be rows rounded up to 128, plus
+ * 128 * groups; the columns behind a group are codes and scales 0.  Offsets
+ * out of range or order are clamped to the rows and to be non-decreasing.
+ */
+int opt2s_mx4_quantize(const opt2s_mx4_source *src, const opt2s_mx4 *q, const opt2s_mx4 *qt,
+                       const int32_t *offsets, int32_t groups, cudaStream_t stream);
+
+/* The values of q, [slabs][rows][cols] contiguous, in one launch (exact in
+ * fp32 and bf16; rounded to nearest in fp16). */
+int opt2s_mx4_dequantize(const opt2s_mx4 *q, void *out, int32_t dtype, cudaStream_t stream);
+
+/*
+ * Products on the tensor cores, sums in fp32, rounded once to `dtype`.  Row i
+ * of an output starts ldd elements behind row i - 1 (ldd >= its columns).
+ * accumulate: 1 adds to what d holds (in fp32, then rounded), 0 overwrites.
+ *
+ * opt2s_mx4_matmul          d[i][j] = sum_k a[i][k] * b[j][k]; slabs 1.
+ * opt2s_mx4_matmul_grouped  rows [offsets[e], offsets[e+1]) of a with slab e
+ *                           of b (b->slabs == groups), as experts' products.
+ *                           Rows in no group are left as they were, or set to
+ *                           zero with fill_rest == 1 (not with accumulate).
+ * opt2s_mx4_matmul_ragged   for each group e a product over the tokens of the
+ *                           group: d[e][i][j] = sum over the group's columns
+ *                           of a[i][.] * b[j][.], a and b the qt of two
+ *                           sources quantised with these offsets; d holds
+ *                           groups * a->rows rows.  An empty group gives
+ *                           zeros.  As the gradients of experts' weights.
+ * One launch each.  An output may not overlap an operand.
+ */
+int opt2s_mx4_matmul(const opt2s_mx4 *a, const opt2s_mx4 *b, void *d, int64_t ldd, int32_t dtype,
+                     int32_t accumulate, cudaStream_t stream);
+int opt2s_mx4_matmul_grouped(const opt2s_mx4 *a, const opt2s_mx4 *b, const int32_t *offsets,
+                             int32_t groups, void *d, int64_t ldd, int32_t dtype,
+                             int32_t accumulate, int32_t fill_rest, cudaStream_t stream);
+int opt2s_mx4_matmul_ragged(const opt2s_mx4 *a, const opt2s_mx4 *b, const int32_t *offsets,
+                            int32_t groups, void *d, int64_t ldd, int32_t dtype,
+                            int32_t accumulate, cudaStream_t stream);
+
+/* CTAs of the products that gave up a bounded wait on the current device
+ * since the library was loaded (0 unless the hardware or the library is at
+ * fault; their outputs are then not written).  Waits for the device. */
+int opt2s_mx4_errors(uint32_t *count);
+
 /* Frees every cached plan of every device (waits for the devices first). */
 int opt2s_release_cache(void);
 
