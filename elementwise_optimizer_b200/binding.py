@@ -100,6 +100,18 @@ class opt2s_mx4_source(ctypes.Structure):
                 ("slab_stride", ctypes.c_int64), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class opt2s_tensor_mx4(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("state1", ctypes.c_void_p),
+                ("state2", ctypes.c_void_p), ("numel", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("slabs", ctypes.c_int64), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("codes_t", ctypes.c_void_p), ("scales_t", ctypes.c_void_p)]
+
+
+class TensorListDescMx4(ctypes.Structure):
+    _fields_ = [("tensors", ctypes.POINTER(opt2s_tensor_mx4)), ("count", ctypes.c_int32)]
+
+
 MX4_BLOCK = 32
 MX4_MAX_GROUPS = 1024
 BLOCK8 = 2048
@@ -167,6 +179,8 @@ EXPORTS = {
                                                ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
                                                ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
                                                ctypes.c_void_p]),
+    "opt2s_step_mx4": (ctypes.c_int, [ctypes.POINTER(TensorListDescMx4), ctypes.POINTER(Hyper), ctypes.c_int,
+                                      ctypes.c_void_p]),
     "opt2s_mx4_errors": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32)]),
     "opt2s_release_cache": (ctypes.c_int, []),
     "opt2s_error_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -355,6 +369,48 @@ class TensorList8:
         return cls(recs)
 
 
+class TensorListMX4:
+    """A marshalled collection for the step that writes 4-bit copies: records
+    (param, grad, state1, state2, numel, dtype_code, (slabs, rows, cols),
+    codes, scales, codes_t, scales_t), pointers as ints (0 for a form that is
+    not kept)."""
+
+    def __init__(self, records: Sequence[tuple]):
+        n = len(records)
+        self._arr = (opt2s_tensor_mx4 * max(n, 1))()
+        for i, (p, g, s1, s2, numel, dt, (slabs, rows, cols), c, s, ct, st) in enumerate(records):
+            self._arr[i] = opt2s_tensor_mx4(p, g, s1, s2, int(numel), int(dt), 0, slabs, rows, cols, c or None,
+                                            s or None, ct or None, st or None)
+        self.desc = TensorListDescMx4(ctypes.cast(self._arr, ctypes.POINTER(opt2s_tensor_mx4)), n)
+        self.count = n
+
+    @classmethod
+    def from_tensors(cls, params, grads, state1, state2, copies) -> "TensorListMX4":
+        """From torch tensors; copies[i] is None, or the pair of MX4Tensors
+        (blocks along the rows, transposed) that the step keeps up to date for
+        a param of 2 dimensions (3 with slabs); either may be None."""
+        recs = []
+        for p, g, s1, s2, pair in zip(params, grads, state1, state2, copies):
+            for t in (p, g, s1, s2):
+                if not t.is_contiguous():
+                    raise ValueError("tensors must be contiguous")
+            if g.dtype != p.dtype or g.numel() != p.numel():
+                raise ValueError("grad must match param in dtype and size")
+            dims, ptrs = (1, 1, 1), [0, 0, 0, 0]
+            if pair is not None and p.numel() > 0:
+                if p.dim() not in (2, 3):
+                    raise ValueError("a param with 4-bit copies has 2 dimensions, or 3 with slabs")
+                dims = (p.shape[0] if p.dim() == 3 else 1, *p.shape[-2:])
+                for i, (q, want) in enumerate(zip(pair, (dims, (dims[0], dims[2], dims[1])))):
+                    if q is None:
+                        continue
+                    if (q.slabs, q.rows, q.cols) != want or q.device != p.device:
+                        raise ValueError(f"copy {q.shape} is not one of a param {tuple(p.shape)} on its device")
+                    ptrs[2 * i:2 * i + 2] = _ptr(q.codes), _ptr(q.scales)
+            recs.append((_ptr(p), _ptr(g), _ptr(s1), _ptr(s2), p.numel(), _torch_dtype_code(p), dims, *ptrs))
+        return cls(recs)
+
+
 def make_hyper(algo: str = "adam", lr: float = 1e-3, beta1: float = 0.9,
                beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 0.0,
                beta3: float = 0.0, alpha: float = 0.0, skip_zeros: bool = False) -> Hyper:
@@ -426,6 +482,13 @@ def opt2s_step_8bit(tl: "TensorList8", hyper: Hyper, step: int, stream=None) -> 
     with fp32 state in the same launch)."""
     check(lib().opt2s_step_8bit(ctypes.byref(tl.desc), ctypes.byref(hyper), int(step),
                                 _stream_handle(stream)), "opt2s_step_8bit")
+
+
+def opt2s_step_mx4(tl: "TensorListMX4", hyper: Hyper, step: int, stream=None) -> None:
+    """opt2s_step that also writes the 4-bit copies of the updated params (one
+    launch for up to 256 tensors)."""
+    check(lib().opt2s_step_mx4(ctypes.byref(tl.desc), ctypes.byref(hyper), int(step),
+                               _stream_handle(stream)), "opt2s_step_mx4")
 
 
 def state_bits_for(numel: int, min_8bit_size: int = MIN_8BIT_SIZE) -> int:

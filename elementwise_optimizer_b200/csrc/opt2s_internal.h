@@ -412,4 +412,23 @@ struct Mx4GemmArgs {
 cudaError_t launch_mx4_gemm(Mx4GemmArgs a, const Mx4GemmOperands& op, cudaStream_t stream);
 cudaError_t mx4_error_count(unsigned int* out);
 
+// A tensor of the step that writes 4-bit copies: with codes or codes_t it is
+// slabs of rows x cols, else numel elements.
+struct StepMx4Rec {
+    void* p;
+    const void* g;
+    float* m;
+    float* v;
+    float* m2;                     // state1 + numel
+    uint8_t *codes, *scales, *codes_t, *scales_t;
+    int64_t numel, slabs, rows, cols;
+    int32_t dtype;
+    int32_t vec;                   // every row of every array starts on 16 bytes
+};
+constexpr int kStepMx4MaxRecs = 256;
+int64_t step_mx4_tiles(const StepMx4Rec& t);
+// One launch over 1 <= n <= kStepMx4MaxRecs non-empty records.
+cudaError_t launch_step_mx4(const StepMx4Rec* recs, int n, int algo, int skip_zeros, StepScalars s,
+                            cudaStream_t stream);
+
 }  // namespace opt2s

@@ -36,8 +36,8 @@ inline void* start_of(const c10::TensorImpl* t)
     return static_cast<char*>(t->storage().data_ptr().get()) + t->storage_offset() * t->itemsize();
 }
 
-// Whether a parameter and its gradient still fit record r (opt2s_tensor or
-// opt2s_tensor8): both defined, dense, contiguous CUDA tensors of the
+// Whether a parameter and its gradient still fit record r (opt2s_tensor,
+// opt2s_tensor8 or opt2s_tensor_mx4): both defined, dense, contiguous CUDA tensors of the
 // record's element count and dtype.
 template <typename Rec>
 inline bool fits(const c10::TensorImpl* p, const c10::TensorImpl* g, const Rec& r)
@@ -58,7 +58,7 @@ inline const c10::TensorImpl* grad_of(const at::Tensor& p)
 }
 
 // Refreshes the param and grad addresses of the `n` records (Rec:
-// opt2s_tensor or opt2s_tensor8) at address `records` from the tensors of
+// opt2s_tensor, opt2s_tensor8 or opt2s_tensor_mx4) at address `records` from the tensors of
 // `params` (record i <-> params[i]).  Returns 0 when no address changed, 1
 // when some did (the records now hold the new ones), and -1 when a parameter
 // has no gradient or no longer fits its record (element count, storage
@@ -101,6 +101,11 @@ int64_t refresh_records8(py::list params, uintptr_t records, int64_t n)
     return refresh<opt2s_tensor8>(params, records, n);
 }
 
+int64_t refresh_records_mx4(py::list params, uintptr_t records, int64_t n)
+{
+    return refresh<opt2s_tensor_mx4>(params, records, n);
+}
+
 }  // namespace
 
 PYBIND11_MODULE(TORCH_EXTENSION_NAME, m)
@@ -109,4 +114,6 @@ PYBIND11_MODULE(TORCH_EXTENSION_NAME, m)
           "Refresh the param/grad addresses of opt2s_tensor records from a parameter list");
     m.def("refresh_records8", &refresh_records8,
           "Refresh the param/grad addresses of opt2s_tensor8 records from a parameter list");
+    m.def("refresh_records_mx4", &refresh_records_mx4,
+          "Refresh the param/grad addresses of opt2s_tensor_mx4 records from a parameter list");
 }

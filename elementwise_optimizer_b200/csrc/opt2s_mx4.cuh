@@ -64,12 +64,13 @@ __device__ __forceinline__ uint32_t encode2(float lo, float hi)
 // the code is c + (f > (r + 0.5)/256).
 __device__ __forceinline__ uint32_t encode_noise(float x, uint32_t r)
 {
+    // each difference below is exact, so the comparison decides on x itself
     const float a = fminf(fabsf(x), 6.0f);
-    const float pos = a < 2.0f ? __fmul_rn(a, 2.0f)
-                               : (a < 4.0f ? __fadd_rn(a, 2.0f) : __fadd_rn(__fmul_rn(a, 0.5f), 4.0f));
+    const float base = a < 2.0f ? 0.0f : (a < 4.0f ? 4.0f : 6.0f);
+    const float pos = a < 2.0f ? __fmul_rn(a, 2.0f) : (a < 4.0f ? __fsub_rn(a, 2.0f) : __fmul_rn(__fsub_rn(a, 4.0f), 0.5f));
     const float c = floorf(pos);
     const float u = __fmul_rn(__fadd_rn(static_cast<float>(r), 0.5f), 1.0f / 256.0f);
-    const uint32_t code = static_cast<uint32_t>(c) + (__fsub_rn(pos, c) > u ? 1u : 0u);
+    const uint32_t code = static_cast<uint32_t>(base + c) + (__fsub_rn(pos, c) > u ? 1u : 0u);
     return code | (__float_as_uint(x) >> 31 << 3);
 }
 

@@ -2,6 +2,8 @@
 // (include/opt2s.h): argument validation and launches.  Nothing here keeps
 // state: a call's tables travel as kernel arguments.
 #include <cstdint>
+#include <new>
+#include <vector>
 
 #include <cuda_runtime.h>
 
@@ -212,6 +214,94 @@ OPT2S_API int opt2s_mx4_matmul_ragged(const opt2s_mx4* a, const opt2s_mx4* b, co
     if (a->cols < 128 * static_cast<int64_t>(groups) || a->cols % 128 != 0) return OPT2S_ERR_INVALID_ARG;
     if (groups * a->rows > kMaxIndex) return OPT2S_ERR_TOO_LARGE;
     return product(a, b, offsets, groups, true, d, groups * a->rows, ldd, dtype, accumulate, 0, stream);
+}
+
+namespace {
+
+// Checks one record of the step, appends its ranges and its kernel record.
+int step_record(const opt2s_tensor_mx4& t, int32_t algo, std::vector<Range>* ranges,
+                std::vector<opt2s::StepMx4Rec>* recs)
+{
+    const opt2s_tensor plain{t.param, t.grad, t.state1, t.state2, t.numel, t.dtype, t.reserved};
+    Range r[8];
+    int k = 0;
+    int st = opt2s::record_ranges(plain, algo, r, &k);
+    if (st != OPT2S_OK || k == 0) return st;
+    size_t n = static_cast<size_t>(k);
+    if (!t.codes != !t.scales || !t.codes_t != !t.scales_t) return OPT2S_ERR_INVALID_ARG;
+    opt2s::StepMx4Rec rec{};
+    rec.p = t.param;
+    rec.g = t.grad;
+    rec.m = t.state1;
+    rec.v = t.state2;
+    rec.m2 = t.state1 + t.numel;
+    rec.numel = t.numel;
+    rec.dtype = t.dtype;
+    if (t.codes || t.codes_t) {
+        if (!good_sizes(t.slabs, t.rows, t.cols) || !good_sizes(t.slabs, t.cols, t.rows)) return OPT2S_ERR_INVALID_ARG;
+        if (t.numel % t.slabs || t.numel / t.slabs % t.rows || t.numel / t.slabs / t.rows != t.cols)
+            return OPT2S_ERR_INVALID_ARG;
+        const opt2s_mx4 q{t.codes, t.scales, t.slabs, t.rows, t.cols};
+        const opt2s_mx4 qt{t.codes_t, t.scales_t, t.slabs, t.cols, t.rows};
+        if (t.codes && (st = matrix_ranges(&q, true, r, &n)) != OPT2S_OK) return st;
+        if (t.codes_t && (st = matrix_ranges(&qt, true, r, &n)) != OPT2S_OK) return st;
+        rec.slabs = t.slabs;
+        rec.rows = t.rows;
+        rec.cols = t.cols;
+        rec.codes = t.codes;
+        rec.scales = t.scales;
+        rec.codes_t = t.codes_t;
+        rec.scales_t = t.scales_t;
+        const int es = opt2s::elem_bytes(t.dtype);
+        rec.vec = t.cols % (16 / es) == 0 && aligned(t.param, 16) && aligned(t.grad, 16) && aligned(t.state1, 16) &&
+                  aligned(t.state2, 16) && (algo == OPT2S_ADAM || t.numel % 4 == 0);
+    }
+    ranges->insert(ranges->end(), r, r + n);
+    recs->push_back(rec);
+    return OPT2S_OK;
+}
+
+int step_mx4(const TensorListDescMx4* desc, const Hyper* hyper, int step, cudaStream_t stream)
+{
+    std::vector<Range> ranges;
+    std::vector<opt2s::StepMx4Rec> recs;
+    ranges.reserve(static_cast<size_t>(desc->count) * 8);
+    recs.reserve(static_cast<size_t>(desc->count));
+    int st;
+    for (int32_t i = 0; i < desc->count; ++i)
+        if ((st = step_record(desc->tensors[i], hyper->algo, &ranges, &recs)) != OPT2S_OK) return st;
+    if ((st = opt2s::overlap_status(ranges.data(), ranges.size())) != OPT2S_OK) return st;
+    const opt2s::StepScalars s = opt2s::make_scalars(hyper, step);
+    constexpr size_t kMost = opt2s::kStepMx4MaxRecs;
+    for (size_t at = 0; at < recs.size(); at += kMost) {        // nothing runs unless every launch can
+        int64_t tiles = 0;
+        for (size_t i = at; i < std::min(recs.size(), at + kMost); ++i) {
+            tiles += opt2s::step_mx4_tiles(recs[i]);
+            if (tiles > INT32_MAX) return OPT2S_ERR_TOO_LARGE;
+        }
+    }
+    for (size_t at = 0; at < recs.size(); at += kMost) {
+        const int n = static_cast<int>(std::min(kMost, recs.size() - at));
+        const cudaError_t e = opt2s::launch_step_mx4(recs.data() + at, n, hyper->algo, hyper->skip_zeros, s, stream);
+        if (e != cudaSuccess) return opt2s::record_cuda_error(e);
+        opt2s::count_launches(1);
+    }
+    return OPT2S_OK;
+}
+
+}  // namespace
+
+OPT2S_API int opt2s_step_mx4(const TensorListDescMx4* desc, const Hyper* hyper, int step, cudaStream_t stream)
+{
+    OPT2S_RANGE("opt2s_step_mx4");
+    const int st = opt2s::validate_hyper(hyper, step);
+    if (st != OPT2S_OK) return st;
+    if (!desc || desc->count < 0 || (desc->count > 0 && !desc->tensors)) return OPT2S_ERR_INVALID_ARG;
+    try {
+        return step_mx4(desc, hyper, step, stream);
+    } catch (const std::bad_alloc&) {
+        return OPT2S_ERR_NO_MEMORY;
+    }
 }
 
 OPT2S_API int opt2s_mx4_errors(uint32_t* count)

@@ -1,0 +1,212 @@
+// opt2s_mx4_step.cu -- the two-state step that also writes the 4-bit copies of
+// the params it updates.
+//
+// A model that multiplies with 4-bit weights needs them again after every
+// step, along their rows and, transposed, down their columns.  Written by the
+// step itself they cost 17/16 byte an element and no second read of the
+// param.  A CTA steps a tile of 128 rows x 64 columns (the element arithmetic
+// of opt2s_device.cuh, so the same bits as opt2s_step), keeps the new params
+// in shared memory as they are stored, and encodes both forms from there.
+// Tensors without copies are stepped in the same launch, 8,192 elements a
+// CTA, a warp on each of eight chunks.  Bound by memory traffic, as the plain
+// step is.
+//
+// The records travel as kernel arguments (up to 256 a launch): no table in
+// device memory, nothing kept between calls, and a captured launch holds all
+// it needs.
+#include "opt2s_device.cuh"
+#include "opt2s_mx4.cuh"
+
+namespace opt2s {
+namespace {
+
+constexpr int kStepThreads = 256;
+constexpr int kStepCols = 64;
+constexpr uint32_t kFlatElems = 8192, kWarpElems = kFlatElems / (kStepThreads / 32);
+
+template <int CAP>
+struct StepMx4Table {
+    int32_t count;
+    int32_t first[CAP + 1];         // tiles of the records before each; [count] is the total
+    StepMx4Rec rec[CAP];
+};
+
+// One element: global memory and, in the tile, its new storage bits.
+template <int DT, int ALGO, bool SKIP>
+__device__ __forceinline__ void step_element(const StepMx4Rec& t, int64_t i, uint8_t* at, const StepScalars& s)
+{
+    using P = Param<DT>;
+    constexpr int B = P::kBytes;
+    uint8_t* p_at = static_cast<uint8_t*>(t.p) + i * B;
+    const float g = P::load1(static_cast<const uint8_t*>(t.g) + i * B, 0);
+    float p = P::load1(p_at, 0);
+    if (!(SKIP && g == 0.0f)) {
+        float m = t.m[i], v = t.v[i], m2 = ALGO == kAdEMAMix ? t.m2[i] : 0.0f;
+        update<ALGO, false>(g, p, m, v, m2, s);
+        P::store1(p_at, 0, p);
+        t.m[i] = m;
+        t.v[i] = v;
+        if (ALGO == kAdEMAMix) t.m2[i] = m2;
+    }
+    P::store1(at, 0, p);
+}
+
+template <int DT, int ALGO, bool SKIP>
+__device__ __forceinline__ void step_tile(const StepMx4Rec& t, int32_t u, uint8_t* tile, const StepScalars& s, int tid)
+{
+    using P = Param<DT>;
+    constexpr int V = P::kVec, kChunks = kStepCols / V, kIters = kTileRows * kChunks / kStepThreads;
+    const int64_t cols = t.cols, rows = t.rows;
+    const int ct = static_cast<int>((cols + 127) / 128 * 2), rt = static_cast<int>((rows + 127) / 128);
+    const int c_at = u % ct, rest = u / ct, r_at = rest % rt;
+    const int64_t slab = rest / rt, row0 = static_cast<int64_t>(r_at) * kTileRows, col0 = static_cast<int64_t>(c_at) * kStepCols;
+    const int n_rows = static_cast<int>(min(static_cast<int64_t>(kTileRows), rows - row0));
+    const int n_cols = static_cast<int>(min(static_cast<int64_t>(kStepCols), cols - col0));      // <= 0: padding only
+    const int64_t base = (slab * rows + row0) * cols + col0;
+
+    if (t.vec) {
+        constexpr int U = 8 / V;            // 8 elements a thread and iteration, as the plain step's vector body
+        for (int it = 0; it < kIters; it += U) {
+            typename P::Raw graw[U], praw[U];
+            float m[U][V], v[U][V], m2[U][V];
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const int x = (it + k) * kStepThreads + tid, r = x / kChunks, c = x % kChunks;
+                if (r < n_rows && c * V < n_cols) {
+                    const int64_t i = base + r * cols + c * V;
+                    graw[k] = P::load(static_cast<const uint8_t*>(t.g) + i * P::kBytes, 0);
+                    praw[k] = P::load(static_cast<const uint8_t*>(t.p) + i * P::kBytes, 0);
+                    load_state<V>(t.m + i, 0, m[k]);
+                    load_state<V>(t.v + i, 0, v[k]);
+                    if (ALGO == kAdEMAMix) load_state<V>(t.m2 + i, 0, m2[k]);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const int x = (it + k) * kStepThreads + tid, r = x / kChunks, c = x % kChunks;
+                typename P::Raw out{};
+                if (r < n_rows && c * V < n_cols) {
+                    const int64_t i = base + r * cols + c * V;
+                    float g[V], p[V];
+                    P::widen(graw[k], g);
+                    P::widen(praw[k], p);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) update<ALGO, SKIP>(g[j], p[j], m[k][j], v[k][j], m2[k][j], s);
+                    out = P::narrow(p, praw[k], g, SKIP);
+                    P::store(static_cast<uint8_t*>(t.p) + i * P::kBytes, 0, out);
+                    store_state<V>(t.m + i, 0, m[k]);
+                    store_state<V>(t.v + i, 0, v[k]);
+                    if (ALGO == kAdEMAMix) store_state<V>(t.m2 + i, 0, m2[k]);
+                }
+                *reinterpret_cast<typename P::Raw*>(tile + tile_chunk<DT, kStepCols>(r, c)) = out;
+            }
+        }
+    } else {
+        for (int x = tid; x < kTileRows * kStepCols; x += kStepThreads) {
+            const int r = x / kStepCols, c = x % kStepCols;
+            uint8_t* at = tile + tile_chunk<DT, kStepCols>(r, c / V) + c % V * P::kBytes;
+            if (r < n_rows && c < n_cols) step_element<DT, ALGO, SKIP>(t, base + r * cols + c, at, s);
+            else P::store1(at, 0, 0.0f);
+        }
+    }
+    __syncthreads();
+    TileOut o{};
+    if (t.codes) {
+        const int64_t rp = (rows + 3) / 4 * 4;
+        o.pitch = (cols + 127) / 128 * 64;
+        o.codes = t.codes + (slab * rows + row0) * o.pitch + c_at * 32;
+        o.scales = t.scales + ((static_cast<int64_t>(c_at / 2) * t.slabs + slab) * rp + row0) * 4 + c_at % 2 * 2;
+        o.rows = n_rows;
+        o.scale_rows = static_cast<int>(min(static_cast<int64_t>(kTileRows), rp - row0));
+        tile_rows_out<DT, kStepCols, false, kStepThreads>(tile, nullptr, o, tid);
+    }
+    if (t.codes_t) {
+        const int64_t cp = (cols + 3) / 4 * 4;
+        o.pitch_t = static_cast<int64_t>(rt) * 64;
+        o.codes_t = t.codes_t + (slab * cols + col0) * o.pitch_t + r_at * 64;
+        o.scales_t = t.scales_t + ((static_cast<int64_t>(r_at) * t.slabs + slab) * cp + col0) * 4;
+        o.cols = n_cols;
+        o.scale_cols = static_cast<int>(min(static_cast<int64_t>(kStepCols), cp - col0));
+        tile_cols_out<DT, kStepCols, false, kStepThreads>(tile, nullptr, o, tid);
+    }
+}
+
+template <int DT, int ALGO, bool SKIP>
+__device__ __forceinline__ void step_flat(const StepMx4Rec& t, int32_t u, const StepScalars& s, int tid)
+{
+    const int64_t at = static_cast<int64_t>(u) * kFlatElems + (tid >> 5) * kWarpElems;
+    if (at >= t.numel) return;
+    ChunkRec c;
+    c.p = static_cast<uint8_t*>(t.p) + at * Param<DT>::kBytes;
+    c.g = static_cast<const uint8_t*>(t.g) + at * Param<DT>::kBytes;
+    c.m = t.m + at;
+    c.v = t.v + at;
+    c.m2 = t.m2 + at;
+    c.len = static_cast<uint32_t>(min(static_cast<int64_t>(kWarpElems), t.numel - at));
+    c.dtype = DT;
+    run_chunk<DT, ALGO, SKIP>(c, s, tid & 31);
+}
+
+template <int DT, int ALGO, bool SKIP>
+__device__ __forceinline__ void step_unit(const StepMx4Rec& t, int32_t u, uint8_t* tile, const StepScalars& s, int tid)
+{
+    if (t.codes || t.codes_t) step_tile<DT, ALGO, SKIP>(t, u, tile, s, tid);
+    else step_flat<DT, ALGO, SKIP>(t, u, s, tid);
+}
+
+template <int CAP, int ALGO, bool SKIP>
+__global__ void __launch_bounds__(kStepThreads)
+step_mx4_kernel(const __grid_constant__ StepMx4Table<CAP> tab, const StepScalars s)
+{
+    __shared__ __align__(128) uint8_t tile[kTileRows * kStepCols * 4];
+    const int32_t b = static_cast<int32_t>(blockIdx.x);
+    const int e = group_of(tab.first, tab.count, b);
+    const StepMx4Rec& t = tab.rec[e];
+    const int32_t u = b - tab.first[e];
+    if (t.dtype == kF32) step_unit<kF32, ALGO, SKIP>(t, u, tile, s, threadIdx.x);
+    else if (t.dtype == kF16) step_unit<kF16, ALGO, SKIP>(t, u, tile, s, threadIdx.x);
+    else step_unit<kBF16, ALGO, SKIP>(t, u, tile, s, threadIdx.x);
+}
+
+template <int CAP>
+cudaError_t launch_cap(const StepMx4Rec* recs, int n, int algo, int skip, const StepScalars& s, cudaStream_t stream)
+{
+    StepMx4Table<CAP> tab;
+    tab.count = n;
+    int64_t total = 0;
+    for (int i = 0; i < n; ++i) {
+        tab.rec[i] = recs[i];
+        tab.first[i] = static_cast<int32_t>(total);
+        total += step_mx4_tiles(recs[i]);
+        if (total > INT32_MAX) return cudaErrorInvalidConfiguration;
+    }
+    tab.first[n] = static_cast<int32_t>(total);
+    const unsigned grid = static_cast<unsigned>(total);
+    if (algo == kAdam) {
+        if (skip) step_mx4_kernel<CAP, kAdam, true><<<grid, kStepThreads, 0, stream>>>(tab, s);
+        else step_mx4_kernel<CAP, kAdam, false><<<grid, kStepThreads, 0, stream>>>(tab, s);
+    } else {
+        if (skip) step_mx4_kernel<CAP, kAdEMAMix, true><<<grid, kStepThreads, 0, stream>>>(tab, s);
+        else step_mx4_kernel<CAP, kAdEMAMix, false><<<grid, kStepThreads, 0, stream>>>(tab, s);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+int64_t step_mx4_tiles(const StepMx4Rec& t)
+{
+    if (t.codes || t.codes_t) return t.slabs * ((t.rows + 127) / 128) * ((t.cols + 127) / 128 * 2);
+    return (t.numel + kFlatElems - 1) / kFlatElems;
+}
+
+cudaError_t launch_step_mx4(const StepMx4Rec* recs, int n, int algo, int skip_zeros, StepScalars s,
+                            cudaStream_t stream)
+{
+    fill_reciprocals(&s);
+    // small collections send small argument blocks
+    return n <= 16 ? launch_cap<16>(recs, n, algo, skip_zeros, s, stream)
+                   : launch_cap<kStepMx4MaxRecs>(recs, n, algo, skip_zeros, s, stream);
+}
+
+}  // namespace opt2s

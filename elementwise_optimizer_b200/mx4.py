@@ -14,8 +14,9 @@ Q cuts its operand into blocks along the contraction, so every matrix of a
 training step is needed in two forms: ``quantize_pair`` makes both from one
 read.  Rounding to 4 bits is to nearest (even), or stochastic from random
 bytes that the caller gives; its gradient is taken as one (straight-through).
-``copies`` skips the weight's quantisation: pass the pair kept from an earlier
-``quantize_pair``.
+``copies`` skips the weight's quantisation: pass the pair that the optimizer
+keeps up to date (``optim.AdamW32bit(..., mx4=True)``, ``mx4_copies(w)``: its
+step writes them, see ``opt2s_step_mx4``), or one from ``quantize_pair``.
 
 All work happens in the kernels of libopt2s.so, on the tensors' device and
 torch's current stream of it; nothing is kept between calls, and every call
@@ -24,15 +25,23 @@ status) or ValueError/TypeError for arguments that do not fit together.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
 
 from . import binding as B
-from .optim import _on_device
+from .binding import TensorListMX4, opt2s_step_mx4  # noqa: F401  (the step that writes the copies)
 
 BLOCK = B.MX4_BLOCK
 MAX_GROUPS = B.MX4_MAX_GROUPS
+
+
+def _on_device(index):
+    """Makes CUDA device `index` current for a launch."""
+    if index == torch._C._cuda_getDevice():
+        return contextlib.nullcontext()
+    return torch.cuda.device(index)
 
 
 def _up(n: int, k: int) -> int:
@@ -110,7 +119,7 @@ def _check_offsets(offsets: torch.Tensor, device) -> int:
     return groups
 
 
-def _quantize(x, noise, offsets, want_q, want_t):
+def _quantize(x, noise, offsets, want_q, want_t, out=None):
     if not x.is_cuda:
         raise ValueError("a tensor to quantise must be on a CUDA device")
     if x.dim() not in (2, 3):
@@ -133,9 +142,15 @@ def _quantize(x, noise, offsets, want_q, want_t):
     src = B.opt2s_mx4_source(x.data_ptr() or None, None if noise is None else noise.data_ptr() or None, slabs, rows,
                              cols, x.stride(-2), x.stride(0) if x.dim() == 3 else 0, dtype, 0)
     lead = x.shape[:-2]
-    q = _empty((*lead, rows, cols), x.device) if want_q else None
     t_cols = _up(rows, 128) + 128 * groups if groups else rows
-    qt = _empty((*lead, cols, t_cols), x.device) if want_t and t_cols else None
+    if out is not None:
+        q, qt = out
+        for m, want in zip(out, ((slabs, rows, cols), (slabs, cols, t_cols))):
+            if (m.slabs, m.rows, m.cols) != want or m.device != x.device:
+                raise ValueError(f"out {m.shape} does not fit a source {tuple(x.shape)} on its device")
+    else:
+        q = _empty((*lead, rows, cols), x.device) if want_q else None
+        qt = _empty((*lead, cols, t_cols), x.device) if want_t and t_cols else None
     with _on_device(x.device.index):
         B.check(B.lib().opt2s_mx4_quantize(
             ctypes.byref(src), ctypes.byref(q._c) if q else None, ctypes.byref(qt._c) if qt else None,
@@ -150,13 +165,15 @@ def quantize(x: torch.Tensor, noise: torch.Tensor | None = None) -> MX4Tensor:
     return _quantize(x.detach(), noise, None, True, False)[0]
 
 
-def quantize_pair(x: torch.Tensor, noise: torch.Tensor | None = None, offsets: torch.Tensor | None = None) -> tuple:
+def quantize_pair(x: torch.Tensor, noise: torch.Tensor | None = None, offsets: torch.Tensor | None = None,
+                  out: tuple | None = None) -> tuple:
     """Both forms of x from one read: (blocks along the last axis, blocks down
     the columns of the transposed matrix).  offsets (int32 on the device,
     groups + 1 values): the rows' groups; the transposed form then starts each
     group at a multiple of 128 columns, as ``matmul_ragged`` reads it.  The
-    second is None for a matrix without rows and offsets."""
-    return _quantize(x.detach(), noise, offsets, True, True)
+    second is None for a matrix without rows and offsets.  out: a pair to
+    write to."""
+    return _quantize(x.detach(), noise, offsets, True, True, out)
 
 
 def _product(name, a, b, d_shape, offsets, dtype, out, accumulate, fill_rest=False):

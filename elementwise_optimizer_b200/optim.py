@@ -29,6 +29,15 @@ weight_decay * param, scaled by the trust ratio ||param|| / ||direction||.
 Like max_unorm it takes four launches per group and step, keeps one record
 per parameter under flatten=True, and is not combined with capturable=True.
 
+mx4=True (or an iterable of parameters) keeps 4-bit copies of the weights for
+the products of ``mx4.linear`` and ``mx4.linear_grouped``: True takes every
+parameter of 2 dimensions, or of 3 (slabs, as experts' weights).
+``mx4_copies(p)`` gives a parameter's pair, and every step writes it anew
+from the updated parameter (opt2s_step_mx4: one launch for up to 256 tensors,
+the parameters and states bit for bit as without copies).  A parameter that
+something else than the step has changed (a loaded state dict) needs
+``refresh_mx4()``.  Not combined with flatten, capturable, max_unorm or lamb.
+
 Without flatten, each group's launch records (the tensors' addresses) are
 built once and refreshed in place every step by a small C++ helper
 (csrc/opt2s_marshal.cpp) that reads the current parameter and gradient
@@ -110,7 +119,7 @@ class TwoStateOptimizer(torch.optim.Optimizer):
                  betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.0,
                  beta3: float = 0.9999, alpha: float = 5.0, skip_zeros: bool = False,
                  capturable: bool = False, table_len: int = 1024, flatten: bool = False,
-                 max_unorm: float = 0.0, lamb: bool = False):
+                 max_unorm: float = 0.0, lamb: bool = False, mx4=False):
         if algo not in B.ALGOS:
             raise ValueError(f"algo must be one of {sorted(B.ALGOS)}")
         if not (0.0 <= max_unorm < float("inf")):
@@ -120,6 +129,8 @@ class TwoStateOptimizer(torch.optim.Optimizer):
         if lamb and (capturable or max_unorm > 0.0 or algo == "ademamix"):
             raise ValueError("lamb takes Adam moments and is not combined with capturable "
                              "or max_unorm")
+        if mx4 is not False and (flatten or capturable or max_unorm > 0.0 or lamb):
+            raise ValueError("mx4 is not combined with flatten, capturable, max_unorm or lamb")
         defaults = dict(lr=lr, betas=tuple(betas), eps=eps, weight_decay=weight_decay,
                         beta3=beta3, alpha=alpha, skip_zeros=skip_zeros)
         self.algo = "ademamix" if algo == "ademamix" else "adam"
@@ -127,9 +138,17 @@ class TwoStateOptimizer(torch.optim.Optimizer):
         self.table_len = int(table_len)
         self.max_unorm = float(max_unorm)
         self.lamb = bool(lamb)
+        self._mx4 = mx4 if isinstance(mx4, bool) else {id(p) for p in mx4}
+        self._mx4_pairs = {}
         super().__init__(params, defaults)
         self._group_cache = {}
         self._flat = None
+        if self._mx4 is not False:
+            self._refresh_fn = "refresh_records_mx4"
+            if self._mx4 is not True:
+                known = {id(p): p for g in self.param_groups for p in g["params"]}
+                if any(i not in known or known[i].dim() not in (2, 3) for i in self._mx4):
+                    raise ValueError("mx4 names parameters of this optimizer with 2 dimensions (3 with slabs)")
         if flatten:
             if capturable:
                 raise ValueError("flatten and capturable are not combined")
@@ -272,6 +291,30 @@ class TwoStateOptimizer(torch.optim.Optimizer):
                     f["counter"].fill_(f["step"])
         self._group_cache = {}
 
+    # ---- 4-bit copies --------------------------------------------------------
+    def _has_mx4(self, p):
+        if self._mx4 is True:
+            return p.dim() in (2, 3) and p.numel() > 0
+        return self._mx4 is not False and id(p) in self._mx4 and p.numel() > 0
+
+    def mx4_copies(self, p):
+        """The pair of 4-bit forms of parameter p that the steps keep up to
+        date (made from p at the first call)."""
+        if not self._has_mx4(p):
+            raise ValueError("this parameter has no 4-bit copies (see the mx4 argument)")
+        pair = self._mx4_pairs.get(p)
+        if pair is None:
+            from . import mx4
+            pair = self._mx4_pairs[p] = mx4.quantize_pair(p)
+        return pair
+
+    def refresh_mx4(self) -> None:
+        """Make every 4-bit copy anew, in place, from its parameter's present
+        value."""
+        from . import mx4
+        for p, pair in self._mx4_pairs.items():
+            mx4.quantize_pair(p, out=pair)
+
     # ---- per-group launch data ------------------------------------------
     def _hyper(self, group):
         b1, b2 = group["betas"]
@@ -351,6 +394,10 @@ class TwoStateOptimizer(torch.optim.Optimizer):
 
     def _records(self, ps, states):
         """The launch records of parameters ps with their states."""
+        if self._mx4 is not False:
+            return B.TensorListMX4.from_tensors(
+                ps, [p.grad for p in ps], [s["state1"] for s in states], [s["state2"] for s in states],
+                [self.mx4_copies(p) if self._has_mx4(p) else None for p in ps])
         return B.TensorList.from_tensors(ps, [p.grad for p in ps], [s["state1"] for s in states],
                                          [s["state2"] for s in states])
 
@@ -399,7 +446,9 @@ class TwoStateOptimizer(torch.optim.Optimizer):
 
     def _launch(self, tl, hyper, step):
         """One step of a group's records (not capturable)."""
-        if self.lamb:
+        if self._mx4 is not False:
+            B.opt2s_step_mx4(tl, hyper, step)
+        elif self.lamb:
             B.opt2s_step_lamb(tl, hyper, step)
         elif self.max_unorm > 0.0:
             B.opt2s_step_max_unorm(tl, hyper, self.max_unorm, step)

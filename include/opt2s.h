@@ -521,6 +521,44 @@ int opt2s_mx4_matmul_ragged(const opt2s_mx4 *a, const opt2s_mx4 *b, const int32_
  * fault; their outputs are then not written).  Waits for the device. */
 int opt2s_mx4_errors(uint32_t *count);
 
+/*
+ * opt2s_step that also writes the 4-bit copies of the params it has updated:
+ * for each record with them, q (codes, scales: blocks along the rows) and/or
+ * qt (codes_t, scales_t: blocks down the columns, transposed) of the new
+ * param, as opt2s_mx4_quantize (nearest) makes them, without a second read
+ * of the param.  A record without copies (all four null) is stepped as
+ * opt2s_step steps it; its slabs, rows and cols are ignored.  Param and
+ * states get opt2s_step's bits.
+ *
+ * slabs * rows * cols == numel, row-major and contiguous.  codes and scales
+ * (codes_t and scales_t) are given together, 16-byte aligned, of
+ * opt2s_mx4_code_bytes / _scale_bytes of (slabs, rows, cols) and (slabs,
+ * cols, rows) bytes.  Validation otherwise as opt2s_step, at every call.
+ * ceil(non-empty records / 256) launches on `stream`; the records travel as
+ * kernel arguments, so nothing is allocated or kept between calls and a
+ * captured launch replays the step with the same `step` number.
+ */
+typedef struct {
+    void *param;
+    const void *grad;
+    float *state1;
+    float *state2;
+    int64_t numel;
+    int32_t dtype;
+    int32_t reserved;               /* must be 0 */
+    int64_t slabs, rows, cols;
+    uint8_t *codes, *scales;
+    uint8_t *codes_t, *scales_t;
+} opt2s_tensor_mx4;
+
+typedef struct {
+    const opt2s_tensor_mx4 *tensors;   /* HOST array of `count` records */
+    int32_t count;
+} TensorListDescMx4;
+
+int opt2s_step_mx4(const TensorListDescMx4 *desc, const Hyper *hyper, int step,
+                   cudaStream_t stream);
+
 /* Frees every cached plan of every device (waits for the devices first). */
 int opt2s_release_cache(void);
 
