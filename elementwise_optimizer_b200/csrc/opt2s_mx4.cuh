@@ -46,31 +46,36 @@ __device__ __forceinline__ float inverse_scale(uint32_t byte)
     return byte == 255u ? 0.0f : __uint_as_float((254u - byte) << 23);
 }
 
-// Two E2M1 codes in one byte, `lo` in the low nibble: nearest, ties to even,
-// magnitudes above 6 saturated.
-__device__ __forceinline__ uint32_t encode2(float lo, float hi)
+// Eight E2M1 codes in a word, x[0] in the lowest nibble: nearest, ties to
+// even, magnitudes above 6 saturated.
+__device__ __forceinline__ uint32_t encode8(float x0, float x1, float x2, float x3, float x4, float x5, float x6,
+                                            float x7)
 {
     uint32_t r;
     asm("{\n\t"
-        ".reg .b8 t;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n\t"
-        "cvt.u32.u8 %0, t;\n\t"
-        "}" : "=r"(r) : "f"(lo), "f"(hi));
+        ".reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t"
+        "}" : "=r"(r) : "f"(x0), "f"(x1), "f"(x2), "f"(x3), "f"(x4), "f"(x5), "f"(x6), "f"(x7));
     return r;
 }
 
-// One E2M1 code rounded stochastically with the byte r: with c + f the
-// position of |x| among the codes' magnitudes (linear between neighbours),
-// the code is c + (f > (r + 0.5)/256).
+// One E2M1 code rounded stochastically with the byte r: the upper of the two
+// neighbouring codes when |x| lies more than (r + 0.5)/256 of the way to it.
+// From 1 on a code is the exponent and one mantissa bit, the way is the other
+// 22 bits, and the comparison is the carry of an addition; below 1 the same
+// holds for 1 + |x|.  That sum is rounded up, which cannot move the way past
+// a threshold (a multiple of 2^13 units of the last bit) that it had not
+// passed, so the comparison is exact for every x.
 __device__ __forceinline__ uint32_t encode_noise(float x, uint32_t r)
 {
-    // each difference below is exact, so the comparison decides on x itself
     const float a = fminf(fabsf(x), 6.0f);
-    const float base = a < 2.0f ? 0.0f : (a < 4.0f ? 4.0f : 6.0f);
-    const float pos = a < 2.0f ? __fmul_rn(a, 2.0f) : (a < 4.0f ? __fsub_rn(a, 2.0f) : __fmul_rn(__fsub_rn(a, 4.0f), 0.5f));
-    const float c = floorf(pos);
-    const float u = __fmul_rn(__fadd_rn(static_cast<float>(r), 0.5f), 1.0f / 256.0f);
-    const uint32_t code = static_cast<uint32_t>(base + c) + (__fsub_rn(pos, c) > u ? 1u : 0u);
+    const bool small = a < 1.0f;
+    const uint32_t y = __float_as_uint(small ? __fadd_ru(a, 1.0f) : a);
+    const uint32_t code = ((y + (0x3FDFFFu - (r << 14))) >> 22) - (small ? 254u : 252u);
     return code | (__float_as_uint(x) >> 31 << 3);
 }
 
@@ -87,67 +92,58 @@ __device__ __forceinline__ float2 decode2(uint32_t byte)
 }
 
 // Storage traits of a 4-bit kernel's source: kPer elements in a 16-byte
-// chunk, unpacked to fp32.
+// chunk; element i of a run of words; for the 16-bit types one half of a
+// word, and the fp32 bits of a magnitude.
 template <int DT> struct Src;
 template <> struct Src<kF32> {
     static constexpr int kPer = 4, kBytes = 4;
-    __device__ static void unpack(const uint4& c, float* x) {
-        x[0] = __uint_as_float(c.x); x[1] = __uint_as_float(c.y);
-        x[2] = __uint_as_float(c.z); x[3] = __uint_as_float(c.w);
-    }
-    __device__ static float one(const void* p, int64_t i) { return static_cast<const float*>(p)[i]; }
+    __device__ static float element(const uint32_t* w, int i) { return __uint_as_float(w[i]); }
+    __device__ static float half(uint32_t w, int) { return __uint_as_float(w); }
+    __device__ static uint32_t magnitude(uint32_t bits) { return bits; }
     __device__ static uint32_t bits(const void* p, int64_t i) { return static_cast<const uint32_t*>(p)[i]; }
 };
 template <> struct Src<kBF16> {
     static constexpr int kPer = 8, kBytes = 2;
-    __device__ static float2 pair(uint32_t w) {
-        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-    }
-    __device__ static void unpack(const uint4& c, float* x) {
-        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) { const float2 f = pair(w[k]); x[2 * k] = f.x; x[2 * k + 1] = f.y; }
-    }
+    __device__ static float half(uint32_t w, int j) { return __uint_as_float(j ? w & 0xFFFF0000u : w << 16); }
+    __device__ static float element(const uint32_t* w, int i) { return half(w[i / 2], i & 1); }
+    __device__ static uint32_t magnitude(uint32_t bits) { return bits << 16; }
     __device__ static uint32_t bits(const void* p, int64_t i) { return static_cast<const uint16_t*>(p)[i]; }
 };
 template <> struct Src<kF16> {
     static constexpr int kPer = 8, kBytes = 2;
-    __device__ static float2 pair(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
-    __device__ static void unpack(const uint4& c, float* x) {
-        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) { const float2 f = pair(w[k]); x[2 * k] = f.x; x[2 * k + 1] = f.y; }
+    __device__ static float half(uint32_t w, int j)
+    {
+        const __half2 h = *reinterpret_cast<const __half2*>(&w);
+        return j ? __high2float(h) : __low2float(h);
     }
+    __device__ static float element(const uint32_t* w, int i) { return half(w[i / 2], i & 1); }
+    __device__ static uint32_t magnitude(uint32_t bits) { return abs_bits(half(bits, 0)); }
     __device__ static uint32_t bits(const void* p, int64_t i) { return static_cast<const uint16_t*>(p)[i]; }
 };
 
-// The scale byte and the 16 bytes of codes of one block.
-template <bool NOISE>
-__device__ __forceinline__ uint4 encode_block(const float (&x)[32], const uint32_t (&noise)[8], uint32_t* scale)
+// The largest magnitude of words of a 16-bit type, each half on its own.
+__device__ __forceinline__ uint32_t amax_halves(uint32_t amax, uint32_t w) { return __vmaxu2(amax, w & 0x7FFF7FFFu); }
+
+// The 16 bytes of codes of a block: get(i) is element i, noise(i) its random
+// byte, `scale` the block's scale byte.
+template <bool NOISE, typename Get, typename Noise>
+__device__ __forceinline__ uint4 encode_block(uint32_t scale, Get get, Noise noise)
 {
-    uint32_t amax = 0;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) amax = max(amax, abs_bits(x[i]));
-    *scale = scale_byte(amax);
-    const float inv = inverse_scale(*scale);
-    const bool dead = *scale == 255u;               // inf * 0 and NaN must not reach the encoder
+    const float inv = inverse_scale(scale);
     uint32_t w[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        uint32_t word = 0;
+        float x[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float a = __fmul_rn(x[8 * k + 2 * i], inv), b = __fmul_rn(x[8 * k + 2 * i + 1], inv);
-            uint32_t byte;
-            if (NOISE) {
-                const uint32_t n = noise[2 * k + i / 2] >> (16 * (i & 1));
-                byte = encode_noise(a, n & 255u) | encode_noise(b, n >> 8 & 255u) << 4;
-            } else {
-                byte = encode2(a, b);
-            }
-            word |= byte << (8 * i);
+        for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(get(8 * k + i), inv);
+        if (NOISE) {
+            w[k] = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[k] |= encode_noise(x[i], noise(8 * k + i)) << (4 * i);
+        } else {
+            w[k] = encode8(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]);
         }
-        w[k] = dead ? 0u : word;
+        if (scale == 255u) w[k] = 0;                 // a NaN block's codes
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
@@ -194,7 +190,8 @@ struct TileOut {
 template <int DT, int TC, bool NOISE, int THREADS>
 __device__ __forceinline__ void tile_rows_out(const uint8_t* tile, const uint8_t* noise, const TileOut& o, int tid)
 {
-    constexpr int H = THREADS / kTileRows, B = TC / 32 / H, P = Src<DT>::kPer, C = 32 / P;
+    using S = Src<DT>;
+    constexpr int H = THREADS / kTileRows, B = TC / 32 / H, C = 2 * S::kBytes;     // 16-byte chunks a block
     static_assert(H * B * 32 == TC, "row parts");
     const int r = tid & 127, part = tid >> 7;
     if (r >= o.scale_rows) return;
@@ -202,11 +199,12 @@ __device__ __forceinline__ void tile_rows_out(const uint8_t* tile, const uint8_t
 #pragma unroll
     for (int b = 0; b < B; ++b) {
         const int blk = part * B + b;
-        float x[32];
-        uint32_t nz[8] = {};
+        uint32_t w[4 * C], nz[8] = {}, amax = 0;
 #pragma unroll
-        for (int c = 0; c < C; ++c)
-            Src<DT>::unpack(*reinterpret_cast<const uint4*>(tile + tile_chunk<DT, TC>(r, blk * C + c)), x + c * P);
+        for (int c = 0; c < C; ++c) {
+            const uint4 v = *reinterpret_cast<const uint4*>(tile + tile_chunk<DT, TC>(r, blk * C + c));
+            w[4 * c] = v.x; w[4 * c + 1] = v.y; w[4 * c + 2] = v.z; w[4 * c + 3] = v.w;
+        }
         if (NOISE) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
@@ -214,8 +212,12 @@ __device__ __forceinline__ void tile_rows_out(const uint8_t* tile, const uint8_t
                 nz[4 * c] = v.x; nz[4 * c + 1] = v.y; nz[4 * c + 2] = v.z; nz[4 * c + 3] = v.w;
             }
         }
-        uint32_t s;
-        const uint4 codes = encode_block<NOISE>(x, nz, &s);
+#pragma unroll
+        for (int i = 0; i < 4 * C; ++i) amax = S::kBytes == 2 ? amax_halves(amax, w[i]) : max(amax, w[i] & 0x7FFFFFFFu);
+        if (S::kBytes == 2) amax = S::magnitude(max(amax & 0xFFFFu, amax >> 16));
+        const uint32_t s = scale_byte(amax);
+        const uint4 codes = encode_block<NOISE>(
+            s, [&](int i) { return S::element(w, i); }, [&](int i) { return nz[i / 4] >> (8 * (i & 3)) & 255u; });
         bytes |= s << (8 * b);
         if (r < o.rows) *reinterpret_cast<uint4*>(o.codes + r * o.pitch + blk * 16) = codes;
     }
@@ -230,36 +232,35 @@ __device__ __forceinline__ void tile_rows_out(const uint8_t* tile, const uint8_t
 template <int DT, int TC, bool NOISE, int THREADS>
 __device__ __forceinline__ void tile_cols_out(const uint8_t* tile, const uint8_t* noise, const TileOut& o, int tid)
 {
-    constexpr int W = 4 / Src<DT>::kBytes, kAcross = TC / W, kTasks = kAcross * 4;
+    using S = Src<DT>;
+    constexpr int W = 4 / S::kBytes, P = S::kPer, kAcross = TC / W, kTasks = kAcross * 4;
     for (int t = tid; t < kTasks; t += THREADS) {
         const int c0 = (t % kAcross) * W, rb = t / kAcross;
         if (c0 >= o.scale_cols) continue;
-        float x[W][32];
-        uint32_t nz[W][8] = {};
+        uint32_t w[32], nz[W][8] = {}, amax = 0;
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
             const int r = rb * 32 + i;
-            constexpr int P = Src<DT>::kPer;
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(
-                tile + tile_chunk<DT, TC>(r, c0 / P) + (c0 % P) * Src<DT>::kBytes);
-            if constexpr (W == 1) {
-                x[0][i] = __uint_as_float(w);
-            } else {
-                const float2 f = Src<DT>::pair(w);
-                x[0][i] = f.x;
-                x[W - 1][i] = f.y;
-            }
+            w[i] = *reinterpret_cast<const uint32_t*>(tile + tile_chunk<DT, TC>(r, c0 / P) + (c0 % P) * S::kBytes);
+            amax = W == 2 ? amax_halves(amax, w[i]) : max(amax, w[i] & 0x7FFFFFFFu);
             if (NOISE) {
                 const uint8_t* np = noise + noise_chunk<TC>(r, c0 / 16) + c0 % 16;
-#pragma unroll
-                for (int j = 0; j < W; ++j) nz[j][i / 4] |= static_cast<uint32_t>(np[j]) << (8 * (i & 3));
+                if (W == 2) {
+                    const uint32_t n = *reinterpret_cast<const uint16_t*>(np);
+                    nz[0][i / 4] |= (n & 255u) << (8 * (i & 3));
+                    nz[W - 1][i / 4] |= (n >> 8) << (8 * (i & 3));
+                } else {
+                    nz[0][i / 4] |= static_cast<uint32_t>(*np) << (8 * (i & 3));
+                }
             }
         }
 #pragma unroll
         for (int j = 0; j < W; ++j) {
             if (c0 + j >= o.scale_cols) break;
-            uint32_t s;
-            const uint4 codes = encode_block<NOISE>(x[j], nz[j], &s);
+            const uint32_t s = scale_byte(W == 2 ? S::magnitude(j ? amax >> 16 : amax & 0xFFFFu) : amax);
+            const uint4 codes = encode_block<NOISE>(
+                s, [&](int i) { return W == 2 ? S::half(w[i], j) : __uint_as_float(w[i]); },
+                [&](int i) { return nz[j][i / 4] >> (8 * (i & 3)) & 255u; });
             if (c0 + j < o.cols) *reinterpret_cast<uint4*>(o.codes_t + (c0 + j) * o.pitch_t + rb * 16) = codes;
             o.scales_t[4 * (c0 + j) + rb] = static_cast<uint8_t>(s);
         }

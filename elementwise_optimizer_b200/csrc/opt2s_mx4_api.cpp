@@ -176,6 +176,7 @@ OPT2S_API int opt2s_mx4_dequantize(const opt2s_mx4* q, void* out, int32_t dtype,
     if (st != OPT2S_OK) return st;
     if (!good_dtype(dtype)) return OPT2S_ERR_INVALID_ARG;
     if (q->rows == 0) return OPT2S_OK;
+    if (q->slabs > 65535 || q->cols > 65535 * int64_t{4096}) return OPT2S_ERR_TOO_LARGE;
     const int es = opt2s::elem_bytes(dtype);
     if (!out || !aligned(out, es)) return OPT2S_ERR_INVALID_ARG;
     r[n++] = span(out, q->slabs * q->rows * q->cols * es, true);

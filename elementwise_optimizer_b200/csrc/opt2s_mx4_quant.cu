@@ -14,60 +14,77 @@ namespace {
 constexpr int kQuantThreads = 256;
 constexpr int kTileCols = 128;
 
-// Loads one tile of the source (zeros outside it) into shared memory.
+// A 16-byte copy from global to shared memory that does not wait; zeros when
+// !in (the address must then still be valid).
+__device__ __forceinline__ void copy16(uint8_t* dst, const void* src, bool in)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                 :: "r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+
+// Starts the load of one tile of the source (zeros outside it) into shared
+// memory; copies_done() waits for it.
 template <int DT, bool NOISE>
 __device__ __forceinline__ void load_tile(const Mx4QuantArgs& a, int64_t row0, int rows, int64_t slab, int64_t col0,
                                           uint8_t* tile, uint8_t* noise, int tid)
 {
     using S = Src<DT>;
-    constexpr int P = S::kPer, kChunks = kTileCols / P;
-    const int64_t base = slab * a.slab_stride + row0 * a.row_stride + col0;
+    constexpr int P = S::kPer, kChunks = kTileCols / P, kStep = kQuantThreads / kChunks;
     const int cols = static_cast<int>(min(static_cast<int64_t>(kTileCols), a.cols - col0));
-    for (int t = tid; t < kTileRows * kChunks; t += kQuantThreads) {
-        const int r = t / kChunks, c = t % kChunks, at = c * P;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (r < rows && at < cols) {
-            const int64_t i = base + r * a.row_stride + at;
-            if (a.vec && at + P <= cols) {
-                v = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.x) + i * S::kBytes);
-            } else {
-                uint32_t w[4] = {0, 0, 0, 0};
+    {
+        const int c = tid % kChunks, at = c * P;
+        const uint8_t* x = static_cast<const uint8_t*>(a.x) + (slab * a.slab_stride + row0 * a.row_stride + col0) * S::kBytes;
+        if (a.vec && cols % P == 0) {
+            const int64_t pitch = a.row_stride * S::kBytes;
+            const uint8_t* p = x + c * 16;
 #pragma unroll
-                for (int k = 0; k < P; ++k)
-                    if (at + k < cols) w[k * S::kBytes / 4] |= S::bits(a.x, i + k) << (S::kBytes == 2 ? 16 * (k & 1) : 0);
-                v = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int r = tid / kChunks; r < kTileRows; r += kStep) {
+                const bool in = r < rows && at < cols;
+                copy16(tile + tile_chunk<DT, kTileCols>(r, c), in ? p + r * pitch : static_cast<const uint8_t*>(a.x), in);
+            }
+        } else {
+            for (int r = tid / kChunks; r < kTileRows; r += kStep) {
+                uint32_t w[4] = {0, 0, 0, 0};
+                if (r < rows) {
+#pragma unroll
+                    for (int k = 0; k < P; ++k)
+                        if (at + k < cols)
+                            w[k * S::kBytes / 4] |= S::bits(x, r * a.row_stride + at + k) << (S::kBytes == 2 ? 16 * (k & 1) : 0);
+                }
+                *reinterpret_cast<uint4*>(tile + tile_chunk<DT, kTileCols>(r, c)) = make_uint4(w[0], w[1], w[2], w[3]);
             }
         }
-        *reinterpret_cast<uint4*>(tile + tile_chunk<DT, kTileCols>(r, c)) = v;
     }
     if (NOISE) {
-        const int64_t nbase = (slab * a.rows + row0) * a.cols + col0;
-        for (int t = tid; t < kTileRows * 8; t += kQuantThreads) {
-            const int r = t / 8, c = t % 8, at = c * 16;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (r < rows && at < cols) {
-                const int64_t i = nbase + r * a.cols + at;
-                if (a.noise_vec && at + 16 <= cols) {
-                    v = *reinterpret_cast<const uint4*>(a.noise + i);
-                } else {
-                    uint32_t w[4] = {0, 0, 0, 0};
+        const int c = tid % 8, at = c * 16;
+        const uint8_t* n = a.noise + (slab * a.rows + row0) * a.cols + col0;
+        if (a.noise_vec && cols % 16 == 0) {
+#pragma unroll
+            for (int r = tid / 8; r < kTileRows; r += kQuantThreads / 8) {
+                const bool in = r < rows && at < cols;
+                copy16(noise + noise_chunk<kTileCols>(r, c), in ? n + r * a.cols + at : a.noise, in);
+            }
+        } else {
+            for (int r = tid / 8; r < kTileRows; r += kQuantThreads / 8) {
+                uint32_t w[4] = {0, 0, 0, 0};
+                if (r < rows) {
 #pragma unroll
                     for (int k = 0; k < 16; ++k)
-                        if (at + k < cols) w[k / 4] |= static_cast<uint32_t>(a.noise[i + k]) << (8 * (k & 3));
-                    v = make_uint4(w[0], w[1], w[2], w[3]);
+                        if (at + k < cols) w[k / 4] |= static_cast<uint32_t>(n[r * a.cols + at + k]) << (8 * (k & 3));
                 }
+                *reinterpret_cast<uint4*>(noise + noise_chunk<kTileCols>(r, c)) = make_uint4(w[0], w[1], w[2], w[3]);
             }
-            *reinterpret_cast<uint4*>(noise + noise_chunk<kTileCols>(r, c)) = v;
         }
     }
 }
+
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // grid: x = column tiles, y = row tiles (of all groups), z = slabs.
 template <int DT, bool NOISE>
 __global__ void __launch_bounds__(kQuantThreads) mx4_quantize_kernel(const Mx4QuantArgs a)
 {
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int32_t start[kMaxGroups + 1], first[kMaxGroups + 1];
     uint8_t* tile = smem;
     uint8_t* noise = smem + kTileRows * kTileCols * Src<DT>::kBytes;
     const int tid = threadIdx.x;
@@ -75,6 +92,8 @@ __global__ void __launch_bounds__(kQuantThreads) mx4_quantize_kernel(const Mx4Qu
     const int64_t rt = blockIdx.y;
     int64_t row0 = rt * kTileRows, row_end = a.rows;
     if (a.offsets) {
+        int32_t* start = reinterpret_cast<int32_t*>(smem);          // the tile's room, until it is loaded
+        int32_t* first = start + kMaxGroups + 1;
         ragged_table(a.offsets, a.groups, a.rows, kTileRows, 1, start, first, tid, kQuantThreads);
         if (rt >= first[a.groups]) {                // behind the last group: only padding of the column form
             row0 = row_end = 0;
@@ -83,9 +102,11 @@ __global__ void __launch_bounds__(kQuantThreads) mx4_quantize_kernel(const Mx4Qu
             row0 = start[e] + (rt - first[e]) * kTileRows;
             row_end = start[e + 1];
         }
+        __syncthreads();
     }
     const int rows = static_cast<int>(min(static_cast<int64_t>(kTileRows), row_end - row0));
     load_tile<DT, NOISE>(a, row0, rows, slab, col0, tile, noise, tid);
+    copies_done();
     __syncthreads();
     TileOut o{};
     const int64_t cg = col0 / 128;                  // 128-column group of the row form
@@ -110,22 +131,27 @@ __global__ void __launch_bounds__(kQuantThreads) mx4_quantize_kernel(const Mx4Qu
     }
 }
 
-// A thread's 8 elements (4 bytes of codes) of one row.
+// 2^(s - 127): s = 0 is the subnormal 2^-127, s = 255 NaN.
+__device__ __forceinline__ float scale_value(uint32_t s)
+{
+    return s == 255u ? __uint_as_float(0x7FC00000u) : (s == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(s << 23));
+}
+
+// grid: x = groups of 4 rows, y = 4,096-column parts, z = slabs.  A thread
+// takes 8 elements (4 bytes of codes) a step.
 template <int DT>
 __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const Mx4DequantArgs a)
 {
-    const int64_t cp = (a.cols + 127) / 128 * 128, per_row = cp / 8;
-    const int64_t total = a.slabs * a.rows * per_row, rp = (a.rows + 3) / 4 * 4;
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; t < total;
-         t += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        const int64_t row = t / per_row, c0 = (t - row * per_row) * 8;
-        if (c0 >= a.cols) continue;
-        const int64_t slab = row / a.rows, r = row - slab * a.rows;
+    constexpr int kRows = 4, kPart = 512 * 8;         // 4 rows of 512 x 8 columns a CTA: 8 steps of 256 threads
+    const int64_t cp = (a.cols + 127) / 128 * 128, rp = (a.rows + 3) / 4 * 4;
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kRows, slab = blockIdx.z, col0 = static_cast<int64_t>(blockIdx.y) * kPart;
+#pragma unroll
+    for (int it = 0; it < kRows * 2; ++it) {
+        const int64_t r = row0 + it / 2, c0 = col0 + ((it & 1) * 256 + threadIdx.x) * 8;
+        if (r >= a.rows || c0 >= a.cols) continue;
+        const int64_t row = slab * a.rows + r;
         const uint32_t w = *reinterpret_cast<const uint32_t*>(a.codes + row * (cp / 2) + c0 / 2);
-        const uint32_t s = a.scales[(((c0 >> 7) * a.slabs + slab) * rp + r) * 4 + ((c0 >> 5) & 3)];
-        // 2^(s - 127): s = 0 is the subnormal 2^-127, s = 255 NaN
-        const float scale = s == 255u ? __uint_as_float(0x7FC00000u)
-                                      : (s == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(s << 23));
+        const float scale = scale_value(a.scales[(((c0 >> 7) * a.slabs + slab) * rp + r) * 4 + ((c0 >> 5) & 3)]);
         float x[8];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -199,11 +225,11 @@ cudaError_t launch_mx4_quantize(const Mx4QuantArgs& a, int dtype, int64_t row_ti
 
 cudaError_t launch_mx4_dequantize(const Mx4DequantArgs& a, int dtype, cudaStream_t stream)
 {
-    const int64_t total = a.slabs * a.rows * ((a.cols + 127) / 128 * 16);
-    const int64_t blocks = std::min<int64_t>((total + 255) / 256, 1 << 20);
-    if (dtype == kF32) mx4_dequantize_kernel<kF32><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a);
-    else if (dtype == kF16) mx4_dequantize_kernel<kF16><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a);
-    else mx4_dequantize_kernel<kBF16><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a);
+    const dim3 grid(static_cast<unsigned>((a.rows + 3) / 4), static_cast<unsigned>((a.cols + 4095) / 4096),
+                    static_cast<unsigned>(a.slabs));
+    if (dtype == kF32) mx4_dequantize_kernel<kF32><<<grid, 256, 0, stream>>>(a);
+    else if (dtype == kF16) mx4_dequantize_kernel<kF16><<<grid, 256, 0, stream>>>(a);
+    else mx4_dequantize_kernel<kBF16><<<grid, 256, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
