@@ -31,7 +31,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libopt2s.so")
 TESTING_LIB = os.path.join(PKG, "libopt2s_testing.so")
 # the optimizer front end's marshalling helper (a PyTorch C++ extension)
-MARSHAL_SRC = os.path.join(PKG, "csrc", "opt2s_marshal.cpp")
+MARSHAL_SRCS = [os.path.join(PKG, "csrc", f) for f in ("opt2s_marshal.cpp", "opt2s_mx4_torch.cpp")]
 MARSHAL_DIR = os.path.join(PKG, "_build")
 MARSHAL_NAME = "opt2s_marshal"
 
@@ -57,7 +57,7 @@ def nvcc() -> str:
 
 
 def stale() -> bool:
-    if not os.path.exists(marshal_path()) or os.path.getmtime(marshal_path()) < os.path.getmtime(MARSHAL_SRC):
+    if not _marshal_fresh():
         return True
     for lib in (LIB, TESTING_LIB):
         if not os.path.exists(lib):
@@ -72,19 +72,25 @@ def marshal_path() -> str:
     return os.path.join(MARSHAL_DIR, MARSHAL_NAME + ".so")
 
 
-def build_marshal(force: bool = False, verbose: bool = False) -> str:
-    """Compile the optimizer's marshalling extension in-tree (host C++ against
-    PyTorch's headers; no device code)."""
+def _marshal_fresh() -> bool:
     out = marshal_path()
-    header = os.path.join(INCLUDE, "opt2s.h")
-    if (not force and os.path.exists(out) and os.path.getmtime(out) >= os.path.getmtime(MARSHAL_SRC)
-            and os.path.getmtime(out) >= os.path.getmtime(header)):
+    return os.path.exists(out) and all(os.path.getmtime(out) >= os.path.getmtime(f)
+                                       for f in MARSHAL_SRCS + [os.path.join(INCLUDE, "opt2s.h")])
+
+
+def build_marshal(force: bool = False, verbose: bool = False) -> str:
+    """Compile the marshalling extension of the optimizer and of the 4-bit
+    layers in-tree (host C++ against PyTorch's headers; no device code)."""
+    out = marshal_path()
+    if not force and _marshal_fresh():
         return out
     os.makedirs(MARSHAL_DIR, exist_ok=True)
     from torch.utils import cpp_extension
     cuda_inc = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
-    cpp_extension.load(name=MARSHAL_NAME, sources=[MARSHAL_SRC], build_directory=MARSHAL_DIR,
-                       extra_cflags=["-O2"], extra_include_paths=[INCLUDE, cuda_inc], verbose=verbose)
+    libs = cpp_extension.library_paths()
+    cpp_extension.load(name=MARSHAL_NAME, sources=MARSHAL_SRCS, build_directory=MARSHAL_DIR,
+                       extra_cflags=["-O2"], extra_include_paths=[INCLUDE, cuda_inc],
+                       extra_ldflags=[f"-L{p}" for p in libs] + ["-lc10_cuda"], verbose=verbose)
     return out
 
 

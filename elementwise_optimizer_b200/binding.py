@@ -241,6 +241,11 @@ def lib() -> ctypes.CDLL:
     return _libs[key]
 
 
+def address_of(L: ctypes.CDLL, name: str) -> int:
+    """The address of an entry point, for extensions that call it directly."""
+    return ctypes.cast(getattr(L, name), ctypes.c_void_p).value
+
+
 @contextlib.contextmanager
 def testing_library():
     """Route every call of this module to the test build of the library

@@ -108,8 +108,11 @@ int64_t refresh_records_mx4(py::list params, uintptr_t records, int64_t n)
 
 }  // namespace
 
+void bind_mx4(py::module& m);      // opt2s_mx4_torch.cpp
+
 PYBIND11_MODULE(TORCH_EXTENSION_NAME, m)
 {
+    bind_mx4(m);
     m.def("refresh_records", &refresh_records,
           "Refresh the param/grad addresses of opt2s_tensor records from a parameter list");
     m.def("refresh_records8", &refresh_records8,

@@ -103,15 +103,22 @@ __device__ __forceinline__ void tmem_st4(uint32_t at, uint32_t a, uint32_t b, ui
                  :: "r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+// TMEM loads wait inside the same statement, so that nothing can use the
+// registers before they are filled.
 __device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t (&r)[16])
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
                    "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-                 : "r"(at));
+                 : "r"(at) : "memory");
 }
-__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_ld4(uint32_t at, uint32_t (&r)[4])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n\ttcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -242,9 +249,9 @@ template <int DT> __device__ __forceinline__ uint32_t pack_out(float lo, float h
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// 16 accumulator columns c0 .. c0+15 of this thread's lane (row of P).
-template <int DT, bool SWAP>
-__device__ __forceinline__ void store16(const Mx4GemmArgs& a, const Tile& t, int lane_row, int c0, const float (&x)[16])
+// Accumulator columns c0 .. c0+N-1 of this thread's lane (row of P).
+template <int N, int DT, bool SWAP>
+__device__ __forceinline__ void store_cols(const Mx4GemmArgs& a, const Tile& t, int lane_row, int c0, const float (&x)[N])
 {
     const int cols = static_cast<int>(a.d_cols);
     if (SWAP) {
@@ -253,7 +260,7 @@ __device__ __forceinline__ void store16(const Mx4GemmArgs& a, const Tile& t, int
         const int col = t.d_col + lane_row;
         if (col >= cols) return;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
+        for (int j = 0; j < N; ++j) {
             if (c0 + j >= t.d_rows) break;
             const int64_t i = (t.d_row + c0 + j) * a.ldd + col;
             store_out<DT>(a.d, i, a.accumulate ? __fadd_rn(load_out<DT>(a.d, i), x[j]) : x[j]);
@@ -263,38 +270,37 @@ __device__ __forceinline__ void store16(const Mx4GemmArgs& a, const Tile& t, int
     if (lane_row >= t.d_rows) return;
     const int col = t.d_col + c0;
     const int64_t i = (t.d_row + lane_row) * a.ldd + col;
-    if (a.vec && !a.accumulate && col + 16 <= cols) {
+    if (a.vec && !a.accumulate && col + N <= cols) {
         if (DT == kF32) {
             float4* d = reinterpret_cast<float4*>(static_cast<float*>(a.d) + i);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) d[k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+            for (int k = 0; k < N / 4; ++k) d[k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
         } else {
             uint4* d = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.d) + i);
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
+            for (int k = 0; k < N / 8; ++k)
                 d[k] = make_uint4(pack_out<DT>(x[8 * k], x[8 * k + 1]), pack_out<DT>(x[8 * k + 2], x[8 * k + 3]),
                                   pack_out<DT>(x[8 * k + 4], x[8 * k + 5]), pack_out<DT>(x[8 * k + 6], x[8 * k + 7]));
         }
         return;
     }
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
+    for (int j = 0; j < N; ++j)
         if (col + j < cols) store_out<DT>(a.d, i + j, a.accumulate ? __fadd_rn(load_out<DT>(a.d, i + j), x[j]) : x[j]);
 }
 
-template <bool SWAP>
-__device__ __forceinline__ void store16_any(const Mx4GemmArgs& a, const Tile& t, int lane_row, int c0, const float (&x)[16])
+template <int N, bool SWAP>
+__device__ __forceinline__ void store_any(const Mx4GemmArgs& a, const Tile& t, int lane_row, int c0, const float (&x)[N])
 {
-    if (a.dtype == kF32) store16<kF32, SWAP>(a, t, lane_row, c0, x);
-    else if (a.dtype == kF16) store16<kF16, SWAP>(a, t, lane_row, c0, x);
-    else store16<kBF16, SWAP>(a, t, lane_row, c0, x);
+    if (a.dtype == kF32) store_cols<N, kF32, SWAP>(a, t, lane_row, c0, x);
+    else if (a.dtype == kF16) store_cols<N, kF16, SWAP>(a, t, lane_row, c0, x);
+    else store_cols<N, kBF16, SWAP>(a, t, lane_row, c0, x);
 }
 
 // ---------------------------------------------------------------------------
 // The kernel.  Cluster of a.split CTAs along the contraction (1: none, and
 // each CTA walks tiles blockIdx.x, + gridDim.x, ...; else each cluster has
-// one tile and its CTAs' partial sums meet in the first one's shared memory,
-// added in rank order).
+// one tile).
 // ---------------------------------------------------------------------------
 template <int BN, bool SWAP>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -495,10 +501,9 @@ mx4_gemm_kernel(const __grid_constant__ Mx4GemmMaps maps, const Mx4GemmArgs a)
                         uint32_t r[16];
                         float x[16];
                         tmem_ld16(tmem + quad + b * BN + c, r);
-                        tmem_ld_wait();
 #pragma unroll
                         for (int j = 0; j < 16; ++j) x[j] = __uint_as_float(r[j]);
-                        store16_any<SWAP>(a, o, lane_row, c, x);
+                        store_any<16, SWAP>(a, o, lane_row, c, x);
                     }
                     fence_before();
                     __syncwarp();
@@ -508,62 +513,64 @@ mx4_gemm_kernel(const __grid_constant__ Mx4GemmMaps maps, const Mx4GemmArgs a)
             } else if (split == 1 && !a.accumulate) {
                 const float zero[16] = {};
 #pragma unroll 1
-                for (int c = 0; c < BN; c += 16) store16_any<SWAP>(a, o, lane_row, c, zero);
+                for (int c = 0; c < BN; c += 16) store_any<16, SWAP>(a, o, lane_row, c, zero);
             }
         }
     }
 
     if (split > 1) {
-        // every CTA of the cluster has finished its MMAs (its epilogue warps
-        // have waited for them), so the stages are free for the partial sums
+        // Partial sums meet by reduce-scatter in distributed shared memory:
+        // the tile's token columns go round the ranks four at a time, each
+        // rank gets the others' partial sums of its columns, adds them in rank
+        // order and stores them.  Columns without a token are not exchanged.
+        // All MMAs of the cluster are done here (every CTA's epilogue warps
+        // have waited for them), so the stages' memory is free.
         __syncthreads();
         cluster_sync();
-        const int t = t0;
-        const bool mine = t < tiles && !abort_flag;
+        const bool mine = t0 < tiles && !abort_flag;
         Tile o{};
-        int lo = 0, hi = 0;
+        int lo = 0, hi = 0, quads = 0;
         if (mine) {
-            o = tile_at<BN, SWAP>(a, start, first, t);
+            o = tile_at<BN, SWAP>(a, start, first, t0);
             k_range(o, &lo, &hi);
+            quads = (min(BN, o.d_rows) + 3) / 4;
         }
         const int lane_row = (warp & 3) * 32 + lane;
-        const uint32_t quad = static_cast<uint32_t>(warp & 3) << 21;
+        const uint32_t acc = tmem + (static_cast<uint32_t>(warp & 3) << 21);
+        constexpr int kQuadBytes = kPRows * 16;
+        const int slots = (BN / 4 + split - 1) / split;
         fence_after();
-        if (warp >= 8 && mine && rank > 0) {
-#pragma unroll 1
-            for (int c = 0; c < BN; c += 16) {
-                uint32_t r[16] = {};
-                if (lo < hi) {
-                    tmem_ld16(tmem + quad + c, r);
-                    tmem_ld_wait();
-                }
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const uint32_t local = codes_at + (((rank - 1) * BN + c + j) * kPRows + lane_row) * 4u;
-                    uint32_t remote;
-                    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(remote) : "r"(local));
-                    asm volatile("st.shared::cluster.u32 [%0], %1;" :: "r"(remote), "r"(r[j]) : "memory");
-                }
+        if (warp >= 8) {
+            for (int g = 0; g < quads; ++g) {
+                const int owner = g % split;
+                if (owner == rank) continue;
+                uint32_t r[4] = {};
+                if (lo < hi) tmem_ld4(acc + 4 * g, r);
+                const uint32_t local = codes_at + (rank * slots + g / split) * kQuadBytes + lane_row * 16;
+                uint32_t remote;
+                asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(owner));
+                asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};"
+                             :: "r"(remote), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
             }
         }
         cluster_sync();
-        if (warp >= 8 && mine && rank == 0) {
-            const float* part = reinterpret_cast<const float*>(smem);
-#pragma unroll 1
-            for (int c = 0; c < BN; c += 16) {
-                uint32_t r[16] = {};
-                float x[16];
-                if (lo < hi) {
-                    tmem_ld16(tmem + quad + c, r);
-                    tmem_ld_wait();
+        if (warp >= 8 && (o.k64 > 0 || !a.accumulate)) {
+            for (int g = rank; g < quads; g += split) {
+                uint32_t r[4] = {};
+                if (lo < hi) tmem_ld4(acc + 4 * g, r);
+                float x[4] = {};
+                for (int q = 0; q < split; ++q) {
+                    float4 v;
+                    if (q == rank)
+                        v = make_float4(__uint_as_float(r[0]), __uint_as_float(r[1]), __uint_as_float(r[2]), __uint_as_float(r[3]));
+                    else
+                        v = *reinterpret_cast<const float4*>(smem + (q * slots + g / split) * kQuadBytes + lane_row * 16);
+                    x[0] = __fadd_rn(x[0], v.x);
+                    x[1] = __fadd_rn(x[1], v.y);
+                    x[2] = __fadd_rn(x[2], v.z);
+                    x[3] = __fadd_rn(x[3], v.w);
                 }
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    x[j] = __uint_as_float(r[j]);
-                    for (int q = 0; q < split - 1; ++q)
-                        x[j] = __fadd_rn(x[j], part[(q * BN + c + j) * kPRows + lane_row]);
-                }
-                if (o.k64 > 0 || !a.accumulate) store16_any<SWAP>(a, o, lane_row, c, x);
+                store_any<4, SWAP>(a, o, lane_row, 4 * g, x);
             }
         }
     }
@@ -680,7 +687,7 @@ cudaError_t launch_mx4_gemm(Mx4GemmArgs a, const Mx4GemmOperands& op, cudaStream
         const int64_t wt = (a.w_rows + kPRows - 1) / kPRows;
         const int64_t xt = (a.x_rows + bn - 1) / bn + (a.offsets ? std::min<int64_t>(a.groups, a.x_rows) : 0);
         const int stages = (a.k64 + 3) / 4, most = bn == 16 ? 8 : 4;
-        while (a.split < most && a.split * 2 <= stages && wt * xt * a.split * 2 <= 2 * sms) a.split *= 2;
+        while (a.split < most && a.split * 2 <= stages && wt * xt * a.split * 2 <= sms) a.split *= 2;
         if (bn == 16) return launch_as<16, true>(a, op, sms, stream);
         if (bn == 32) return launch_as<32, true>(a, op, sms, stream);
         return launch_as<64, true>(a, op, sms, stream);
