@@ -92,7 +92,7 @@ int product(const opt2s_mx4* a, const opt2s_mx4* b, const int32_t* offsets, int3
     g.accumulate = accumulate;
     g.fill_rest = fill_rest;
     g.dtype = dtype;
-    g.vec = aligned(d, 16) && ldd * es % 16 == 0;
+    g.vec = aligned(d, 32) && ldd * es % 32 == 0;
     const cudaError_t e = opt2s::launch_mx4_gemm(g, {operand(a), operand(b)}, stream);
     if (e == cudaErrorInvalidConfiguration) return OPT2S_ERR_TOO_LARGE;
     if (e != cudaSuccess) return opt2s::record_cuda_error(e);

@@ -103,21 +103,34 @@ __device__ __forceinline__ void tmem_st4(uint32_t at, uint32_t a, uint32_t b, ui
                  :: "r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// TMEM loads wait inside the same statement, so that nothing can use the
-// registers before they are filled.
-__device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t (&r)[16])
+// TMEM loads of consecutive columns of the thread's lane.  They wait inside
+// the same statement, so that nothing can use the registers before they are
+// filled.
+__device__ __forceinline__ void tmem_ld(uint32_t at, float (&x)[4])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n\ttcgen05.wait::ld.sync.aligned;"
+                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void tmem_ld(uint32_t at, float (&x)[16])
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
                  "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
                  "tcgen05.wait::ld.sync.aligned;"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]),
+                   "=f"(x[8]), "=f"(x[9]), "=f"(x[10]), "=f"(x[11]), "=f"(x[12]), "=f"(x[13]), "=f"(x[14]), "=f"(x[15])
                  : "r"(at) : "memory");
 }
-__device__ __forceinline__ void tmem_ld4(uint32_t at, uint32_t (&r)[4])
+__device__ __forceinline__ void tmem_ld(uint32_t at, float (&x)[32])
 {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n\ttcgen05.wait::ld.sync.aligned;"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]),
+                   "=f"(x[8]), "=f"(x[9]), "=f"(x[10]), "=f"(x[11]), "=f"(x[12]), "=f"(x[13]), "=f"(x[14]), "=f"(x[15]),
+                   "=f"(x[16]), "=f"(x[17]), "=f"(x[18]), "=f"(x[19]), "=f"(x[20]), "=f"(x[21]), "=f"(x[22]), "=f"(x[23]),
+                   "=f"(x[24]), "=f"(x[25]), "=f"(x[26]), "=f"(x[27]), "=f"(x[28]), "=f"(x[29]), "=f"(x[30]), "=f"(x[31])
+                 : "r"(at) : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -144,7 +157,13 @@ constexpr int round_up(int x, int k) { return (x + k - 1) / k * k; }
 template <int BN>
 struct Geo {
     static constexpr int kStages = BN == 256 ? 4 : 5;
-    static constexpr int kAccBufs = BN == 256 ? 1 : 2;
+    // Two accumulators.  At BN = 256 they overlap by 96 of TMEM's columns
+    // (the scales need the rest): the epilogue takes those columns into
+    // registers first and hands them back at once, so the next tile's MMAs
+    // wait for 96 columns to be read, not for the tile to be stored.
+    static constexpr int kAccStep = BN == 256 ? 160 : BN;
+    static constexpr int kOverlap = BN - kAccStep;
+    static constexpr int kAccLag = kOverlap ? 1 : 2;            // a tile's MMAs wait for the epilogue of the tile this many before
     static constexpr int kSfP = 132;                            // words a scale box has per 128-column group
     static constexpr int kSfQ = BN == 256 ? 256 : BN + 4;
     static constexpr int kCodesP = kPRows * 128, kCodesQ = BN * 128;
@@ -156,7 +175,7 @@ struct Geo {
     static constexpr int kSmem = kStages * (kStageCodes + kStageScales) + 1024;
     static constexpr int kQCols = BN < 128 ? 4 : BN / 32;       // TMEM columns of one group's Q scales
     static constexpr int kSfCols = 8 + 2 * kQCols;
-    static constexpr int kSfBase = kAccBufs * BN;
+    static constexpr int kSfBase = kAccStep + BN;
     static constexpr int kUsedCols = kSfBase + kStages * kSfCols;
     static constexpr int kTmemCols = kUsedCols <= 128 ? 128 : (kUsedCols <= 256 ? 256 : 512);
     static_assert(kUsedCols <= 512, "TMEM columns");
@@ -249,6 +268,14 @@ template <int DT> __device__ __forceinline__ uint32_t pack_out(float lo, float h
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// A 32-byte store to a 32-byte aligned address.
+__device__ __forceinline__ void store32(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e, uint32_t f,
+                                        uint32_t g, uint32_t h)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 :: "l"(p), "r"(a), "r"(b), "r"(c), "r"(d), "r"(e), "r"(f), "r"(g), "r"(h) : "memory");
+}
+
 // Accumulator columns c0 .. c0+N-1 of this thread's lane (row of P).
 template <int N, int DT, bool SWAP>
 __device__ __forceinline__ void store_cols(const Mx4GemmArgs& a, const Tile& t, int lane_row, int c0, const float (&x)[N])
@@ -270,17 +297,23 @@ __device__ __forceinline__ void store_cols(const Mx4GemmArgs& a, const Tile& t, 
     if (lane_row >= t.d_rows) return;
     const int col = t.d_col + c0;
     const int64_t i = (t.d_row + lane_row) * a.ldd + col;
-    if (a.vec && !a.accumulate && col + N <= cols) {
+    if (N >= 16 && a.vec && !a.accumulate && col + N <= cols) {
+        // whole 32-byte sectors a lane
         if (DT == kF32) {
-            float4* d = reinterpret_cast<float4*>(static_cast<float*>(a.d) + i);
+            uint32_t* d = static_cast<uint32_t*>(a.d) + i;
 #pragma unroll
-            for (int k = 0; k < N / 4; ++k) d[k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+            for (int k = 0; k < N; k += 8)
+                store32(d + k, __float_as_uint(x[k]), __float_as_uint(x[k + 1]), __float_as_uint(x[k + 2]),
+                        __float_as_uint(x[k + 3]), __float_as_uint(x[k + 4]), __float_as_uint(x[k + 5]),
+                        __float_as_uint(x[k + 6]), __float_as_uint(x[k + 7]));
         } else {
-            uint4* d = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.d) + i);
+            uint16_t* d = static_cast<uint16_t*>(a.d) + i;
 #pragma unroll
-            for (int k = 0; k < N / 8; ++k)
-                d[k] = make_uint4(pack_out<DT>(x[8 * k], x[8 * k + 1]), pack_out<DT>(x[8 * k + 2], x[8 * k + 3]),
-                                  pack_out<DT>(x[8 * k + 4], x[8 * k + 5]), pack_out<DT>(x[8 * k + 6], x[8 * k + 7]));
+            for (int k = 0; k < N; k += 16)
+                store32(d + k, pack_out<DT>(x[k], x[k + 1]), pack_out<DT>(x[k + 2], x[k + 3]),
+                        pack_out<DT>(x[k + 4], x[k + 5]), pack_out<DT>(x[k + 6], x[k + 7]),
+                        pack_out<DT>(x[k + 8], x[k + 9]), pack_out<DT>(x[k + 10], x[k + 11]),
+                        pack_out<DT>(x[k + 12], x[k + 13]), pack_out<DT>(x[k + 14], x[k + 15]));
         }
         return;
     }
@@ -403,10 +436,13 @@ mx4_gemm_kernel(const __grid_constant__ Mx4GemmMaps maps, const Mx4GemmArgs a)
                 int lo, hi;
                 k_range(o, &lo, &hi);
                 if (lo >= hi) continue;                  // nothing to sum: the epilogue takes zeros
-                const int b = n % G::kAccBufs;
-                if (n >= G::kAccBufs && !(ok = bar_wait(acc_empty(b), (n / G::kAccBufs - 1) & 1, &abort_flag))) break;
+                const int b = n & 1;
+                if (n >= G::kAccLag) {
+                    const uint32_t m = n - G::kAccLag;
+                    if (!(ok = bar_wait(acc_empty(m & 1), (m >> 1) & 1, &abort_flag))) break;
+                }
                 fence_after();
-                const uint32_t d = tmem + b * BN;
+                const uint32_t d = tmem + b * G::kAccStep;
                 for (int k = lo; k < hi; k += 4, ++it) {
                     const int s = it % G::kStages;
                     const uint32_t ph = (it / G::kStages) & 1;
@@ -492,22 +528,36 @@ mx4_gemm_kernel(const __grid_constant__ Mx4GemmMaps maps, const Mx4GemmArgs a)
             int lo, hi;
             k_range(o, &lo, &hi);
             if (lo < hi) {
-                const int b = n % G::kAccBufs;
-                if (!warp_wait(acc_full(b), (n / G::kAccBufs) & 1, &abort_flag)) break;
+                const int b = n & 1;
+                if (!warp_wait(acc_full(b), (n >> 1) & 1, &abort_flag)) break;
                 fence_after();
                 if (split == 1) {
-#pragma unroll 1
-                    for (int c = 0; c < BN; c += 16) {
-                        uint32_t r[16];
-                        float x[16];
-                        tmem_ld16(tmem + quad + b * BN + c, r);
+                    const uint32_t acc = tmem + quad + b * G::kAccStep;
+                    constexpr int kChunk = BN < 32 ? 16 : 32, kFirst = G::kOverlap / 32;
+                    // the shared columns first: the last ones of accumulator 0, the first ones of 1
+                    const int c0 = b == 0 ? BN - G::kOverlap : 0;
+                    if constexpr (kFirst > 0) {
+                        float x[kFirst][32];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) x[j] = __uint_as_float(r[j]);
-                        store_any<16, SWAP>(a, o, lane_row, c, x);
+                        for (int i = 0; i < kFirst; ++i) tmem_ld(acc + c0 + 32 * i, x[i]);
+                        fence_before();
+                        __syncwarp();
+                        if (lane == 0) bar_arrive(acc_empty(b));
+#pragma unroll
+                        for (int i = 0; i < kFirst; ++i) store_any<32, SWAP>(a, o, lane_row, c0 + 32 * i, x[i]);
                     }
-                    fence_before();
-                    __syncwarp();
-                    if (lane == 0) bar_arrive(acc_empty(b));
+#pragma unroll 1
+                    for (int i = kFirst; i < BN / kChunk; ++i) {
+                        const int c = (c0 + kChunk * i) % BN;
+                        float x[kChunk];
+                        tmem_ld(acc + c, x);
+                        store_any<kChunk, SWAP>(a, o, lane_row, c, x);
+                    }
+                    if constexpr (kFirst == 0) {
+                        fence_before();
+                        __syncwarp();
+                        if (lane == 0) bar_arrive(acc_empty(b));
+                    }
                 }
                 ++n;
             } else if (split == 1 && !a.accumulate) {
@@ -544,25 +594,24 @@ mx4_gemm_kernel(const __grid_constant__ Mx4GemmMaps maps, const Mx4GemmArgs a)
             for (int g = 0; g < quads; ++g) {
                 const int owner = g % split;
                 if (owner == rank) continue;
-                uint32_t r[4] = {};
-                if (lo < hi) tmem_ld4(acc + 4 * g, r);
+                float r[4] = {};
+                if (lo < hi) tmem_ld(acc + 4 * g, r);
                 const uint32_t local = codes_at + (rank * slots + g / split) * kQuadBytes + lane_row * 16;
                 uint32_t remote;
                 asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(owner));
-                asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};"
-                             :: "r"(remote), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+                asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};"
+                             :: "r"(remote), "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]) : "memory");
             }
         }
         cluster_sync();
         if (warp >= 8 && (o.k64 > 0 || !a.accumulate)) {
             for (int g = rank; g < quads; g += split) {
-                uint32_t r[4] = {};
-                if (lo < hi) tmem_ld4(acc + 4 * g, r);
-                float x[4] = {};
+                float r[4] = {}, x[4] = {};
+                if (lo < hi) tmem_ld(acc + 4 * g, r);
                 for (int q = 0; q < split; ++q) {
                     float4 v;
                     if (q == rank)
-                        v = make_float4(__uint_as_float(r[0]), __uint_as_float(r[1]), __uint_as_float(r[2]), __uint_as_float(r[3]));
+                        v = make_float4(r[0], r[1], r[2], r[3]);
                     else
                         v = *reinterpret_cast<const float4*>(smem + (q * slots + g / split) * kQuadBytes + lane_row * 16);
                     x[0] = __fadd_rn(x[0], v.x);
