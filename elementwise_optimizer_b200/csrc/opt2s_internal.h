@@ -402,12 +402,12 @@ struct Mx4GemmArgs {
     int64_t x_rows;             // token rows (ragged contraction: tokens)
     int64_t w_rows, w_sf_rows;  // weight rows a slab has, and scale rows
     int64_t p_rows;             // ragged contraction: rows of each D
-    int64_t d_cols;
+    int64_t d_rows, d_cols;     // of D, all groups
     int32_t groups;
     int32_t k64;                // 64-element steps of the contraction
     int32_t ragged_k;           // the groups cut the contraction
     int32_t accumulate, fill_rest, dtype, vec;
-    int32_t split, tiles, w_tiles, p_tiles, q_tiles;    // set by the launch
+    int32_t split, tiles, w_tiles, p_tiles, q_tiles, tma_store;    // set by the launch
 };
 cudaError_t launch_mx4_gemm(Mx4GemmArgs a, const Mx4GemmOperands& op, cudaStream_t stream);
 cudaError_t mx4_error_count(unsigned int* out);

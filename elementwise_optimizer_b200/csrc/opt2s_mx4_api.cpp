@@ -86,6 +86,7 @@ int product(const opt2s_mx4* a, const opt2s_mx4* b, const int32_t* offsets, int3
     g.w_rows = b->rows;
     g.w_sf_rows = up(b->rows, 4);
     g.p_rows = a->rows;
+    g.d_rows = d_rows;
     g.d_cols = b->rows;
     g.k64 = static_cast<int32_t>((a->cols + 63) / 64);
     g.ragged_k = ragged;

@@ -5,11 +5,11 @@
 // a tile of 128 rows of P by BN rows of Q:
 //   warp 0      moves tiles of codes (128-byte swizzled rows of 256 elements)
 //               and of scales into a ring of shared-memory stages with TMA;
-//   warps 4-7   copy a stage's scale words from shared memory into TMEM, in
-//               the layout the block-scaled MMA reads (row r of 32 in lane r
-//               of every quadrant, 4 blocks to a 32-bit column);
-//   warp 1      issues the MMAs, 64 elements of the contraction each, into an
-//               fp32 accumulator in TMEM;
+//   warps 4-7   bring a stage's scale words, in shared memory, into the order
+//               in which they are copied to TMEM, a warp every fourth stage;
+//   warp 1      issues the copies of the scales to TMEM and the MMAs, 64
+//               elements of the contraction each, into an fp32 accumulator in
+//               TMEM;
 //   warps 8-11  read finished accumulators and store them.
 // Scales are stored by 128-column group, [group][row][4 bytes], so a tile's
 // scales are contiguous whatever row it starts at: groups of rows that begin
@@ -57,10 +57,27 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
     return done != 0;
 }
 
+__device__ __forceinline__ uint32_t in_rank(uint32_t addr, int rank)      // addr in another CTA of the cluster
+{
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void bar_arrive_cluster(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
+}
+
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // Bounded wait; false when it ran out or the CTA is aborting.
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag)
 {
-    if (bar_try(bar, parity)) return true;
     for (uint32_t i = 0; i < kWaitLimit; ++i) {
         if (bar_try(bar, parity)) return true;
         if ((i & 255u) == 255u && *abort_flag) return false;
@@ -76,31 +93,61 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
     return __all_sync(0xFFFFFFFFu, bar_wait(bar, parity, abort_flag));
 }
 
+// A tile into this CTA's shared memory; PAIR: `bar` may be the other CTA's.
+template <bool PAIR = false>
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar)
 {
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-                 " [%0], [%1, {%2, %3}], [%4];"
-                 :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+    if (PAIR)
+        asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                     " [%0], [%1, {%2, %3}], [%4];"
+                     :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                     " [%0], [%1, {%2, %3}], [%4];"
+                     :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, uint32_t src)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];\n\t"
+                 "cp.async.bulk.commit_group;" :: "l"(map), "r"(x), "r"(y), "r"(src) : "memory");
 }
 
+// Arrives at `bar` (PAIR: in both CTAs) when the MMAs issued so far are done.
+template <bool PAIR>
 __device__ __forceinline__ void mma_commit(uint32_t bar)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar) : "memory");
+    if (PAIR)
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                     :: "r"(bar), "h"(static_cast<uint16_t>(3)) : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar) : "memory");
 }
 
+template <bool PAIR>
 __device__ __forceinline__ void mma_mx4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
                                         uint32_t accumulate)
 {
-    asm volatile("{\n\t.reg .pred p;\n\t"
-                 "setp.ne.b32 p, %6, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-                 :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
+    if (PAIR)
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "setp.ne.b32 p, %6, 0;\n\t"
+                     "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+                     :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "setp.ne.b32 p, %6, 0;\n\t"
+                     "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+                     :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
 }
 
-__device__ __forceinline__ void tmem_st4(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+// 512 bytes of scales, [32][4] words, to four TMEM columns: word [r][j] to lane
+// r (and 32 + r, 64 + r, 96 + r) of column j.  PAIR: in both CTAs.  In order
+// with the MMAs that the thread issues after it.
+template <bool PAIR>
+__device__ __forceinline__ void copy_scales(uint32_t tmem_col, uint32_t addr)
 {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};"
-                 :: "r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+    const uint64_t desc = static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(128 >> 4) << 32 | 1ull << 46;
+    if (PAIR) asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" :: "r"(tmem_col), "l"(desc) : "memory");
+    else asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" :: "r"(tmem_col), "l"(desc) : "memory");
 }
 
 // TMEM loads of consecutive columns of the thread's lane.  They wait inside
@@ -132,7 +179,6 @@ __device__ __forceinline__ void tmem_ld(uint32_t at, float (&x)[32])
                    "=f"(x[24]), "=f"(x[25]), "=f"(x[26]), "=f"(x[27]), "=f"(x[28]), "=f"(x[29]), "=f"(x[30]), "=f"(x[31])
                  : "r"(at) : "memory");
 }
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
@@ -154,9 +200,9 @@ __device__ __forceinline__ uint64_t tile_desc(uint32_t addr)
 // ---------------------------------------------------------------------------
 constexpr int round_up(int x, int k) { return (x + k - 1) / k * k; }
 
-template <int BN>
+template <int BN, bool SWAP, bool PAIR>
 struct Geo {
-    static constexpr int kStages = BN == 256 ? 4 : 5;
+    static constexpr int kStages = 5;
     // Two accumulators.  At BN = 256 they overlap by 96 of TMEM's columns
     // (the scales need the rest): the epilogue takes those columns into
     // registers first and hands them back at once, so the next tile's MMAs
@@ -164,25 +210,30 @@ struct Geo {
     static constexpr int kAccStep = BN == 256 ? 160 : BN;
     static constexpr int kOverlap = BN - kAccStep;
     static constexpr int kAccLag = kOverlap ? 1 : 2;            // a tile's MMAs wait for the epilogue of the tile this many before
+    static constexpr int kQRows = PAIR ? BN / 2 : BN;           // rows of Q's codes a CTA holds
     static constexpr int kSfP = 132;                            // words a scale box has per 128-column group
     static constexpr int kSfQ = BN == 256 ? 256 : BN + 4;
-    static constexpr int kCodesP = kPRows * 128, kCodesQ = BN * 128;
+    static constexpr int kCodesP = kPRows * 128, kCodesQ = kQRows * 128;
     static constexpr int kScalesP = kSfP * 8, kScalesQ = kSfQ * 8;
-    static constexpr int kTx = kCodesP + kCodesQ + kScalesP + kScalesQ;
+    static constexpr int kTxCodes = kCodesP + kCodesQ, kTxScales = kScalesP + kScalesQ;
     static constexpr int kStageCodes = kCodesP + round_up(kCodesQ, 1024);
-    static constexpr int kStageScales = round_up(kScalesP, 128) + round_up(kScalesQ, 128);
+    static constexpr int kQAtoms = BN <= 128 ? 1 : BN / 128;    // 128-row pieces of Q's scales
+    static constexpr int kStageScales = round_up(kScalesP, 128) + (kScalesQ > 1024 ? round_up(kScalesQ, 128) : 1024);
     static constexpr int kScalesQAt = round_up(kScalesP, 128);  // where a stage's Q scales start
-    static constexpr int kSmem = kStages * (kStageCodes + kStageScales) + 1024;
-    static constexpr int kQCols = BN < 128 ? 4 : BN / 32;       // TMEM columns of one group's Q scales
+    static constexpr int kOutBytes = SWAP ? 0 : 4 * 2 * 4096;   // two 32-row x 128-byte store buffers an epilogue warp
+    static constexpr int kSmem = kStages * (kStageCodes + kStageScales) + kOutBytes + 1024;
+    static constexpr int kQCols = 4 * kQAtoms;                  // TMEM columns of one group's Q scales
     static constexpr int kSfCols = 8 + 2 * kQCols;
+    static constexpr int kSfSlots = BN == 256 ? 4 : kStages;
     static constexpr int kSfBase = kAccStep + BN;
-    static constexpr int kUsedCols = kSfBase + kStages * kSfCols;
+    static constexpr int kUsedCols = kSfBase + kSfSlots * kSfCols;
     static constexpr int kTmemCols = kUsedCols <= 128 ? 128 : (kUsedCols <= 256 ? 256 : 512);
     static_assert(kUsedCols <= 512, "TMEM columns");
+    static_assert(kSmem + 2 * 4 * (kMaxGroups + 1) + 512 <= 232448, "shared memory");
 };
 
 struct Mx4GemmMaps {
-    CUtensorMap p_codes, q_codes, p_scales, q_scales;
+    CUtensorMap p_codes, q_codes, p_scales, q_scales, d;
 };
 
 // Elements of the contraction per stage: 256, one 128-byte row of codes (two
@@ -199,19 +250,22 @@ struct Tile {
     int d_col;             // first column of D
 };
 
-template <int BN, bool SWAP>
-__device__ __forceinline__ Tile tile_at(const Mx4GemmArgs& a, const int32_t* start, const int32_t* first, int t)
+// Tile t as CTA `half` of a pair sees it (0 without pairs): its 128 rows of P.
+template <int BN, bool SWAP, bool PAIR>
+__device__ __forceinline__ Tile tile_at(const Mx4GemmArgs& a, const int32_t* start, const int32_t* first, int t, int half)
 {
+    constexpr int kP = PAIR ? 2 * kPRows : kPRows;
     Tile o;
     if (a.ragged_k) {
         const int per = a.p_tiles * a.q_tiles, e = t / per, u = t - e * per;
         const int pi = u % a.p_tiles, qi = u / a.p_tiles;
-        o.p_row = o.p_sf = pi * kPRows;
-        o.q_row = o.q_sf = qi * BN;
+        o.p_row = o.p_sf = pi * kP + half * kPRows;
+        o.q_sf = qi * BN;
+        o.q_row = o.q_sf + half * (BN / 2);
         o.kg0 = first[e];
         o.k64 = (start[e + 1] - start[e] + 63) / 64;
-        o.d_row = e * a.p_rows + pi * kPRows;
-        o.d_rows = static_cast<int>(a.p_rows) - pi * kPRows;
+        o.d_row = e * a.p_rows + o.p_row;
+        o.d_rows = static_cast<int>(a.p_rows) - o.p_row;
         o.d_col = qi * BN;
         return o;
     }
@@ -222,17 +276,17 @@ __device__ __forceinline__ Tile tile_at(const Mx4GemmArgs& a, const int32_t* sta
         x0 = start[e];
         x1 = start[e + 1];
     }
-    constexpr int kX = SWAP ? BN : kPRows, kW = SWAP ? kPRows : BN;
+    constexpr int kX = SWAP ? BN : kP, kW = SWAP ? kPRows : BN;
     // weight tiles inside bands of kBand token tiles, so that neighbouring CTAs share both operands in L2
     constexpr int kBand = 8;
     const int xt = (x1 - x0 + kX - 1) / kX, wt = a.w_tiles;
     const int band = u / (kBand * wt), in = u - band * kBand * wt;
     const int height = min(kBand, xt - band * kBand);
     const int xi = band * kBand + in % height, wi = in / height;
-    const int xr = x0 + xi * kX, wr = wi * kW;
+    const int xr = x0 + xi * kX + half * kPRows, wr = wi * kW;
     const int w_row = e * static_cast<int>(a.w_rows) + wr, w_sf = e * static_cast<int>(a.w_sf_rows) + wr;
     o.p_row = SWAP ? w_row : xr;
-    o.q_row = SWAP ? xr : w_row;
+    o.q_row = SWAP ? xr : w_row + half * (BN / 2);
     o.p_sf = SWAP ? w_sf : xr;
     o.q_sf = SWAP ? xr : w_sf;
     o.kg0 = 0;
@@ -330,41 +384,119 @@ __device__ __forceinline__ void store_any(const Mx4GemmArgs& a, const Tile& t, i
     else store_cols<N, kBF16, SWAP>(a, t, lane_row, c0, x);
 }
 
+// An epilogue warp's two buffers of 32 rows x 128 bytes (swizzled as the
+// output's tensor map expects), each stored by TMA in whole lines: direct
+// stores, 32 bytes a lane in 32 different rows, took longer than a main loop
+// of 2,048 (80 us against 62 us for 8192 x 8192 x 2048).
+struct StoreBuffers {
+    uint8_t* base;
+    uint32_t used = 0;
+    bool pending = false;
+    __device__ explicit StoreBuffers(uint8_t* at) : base(at) {}
+
+    // 32 columns c .. c+31 (c a multiple of 32) of the warp's 32 rows, all of
+    // which exist; the map's bounds cut columns behind D's last.  fp32 fills a
+    // buffer with one call, 16-bit outputs with two, in either order: c and
+    // c ^ 32.
+    __device__ __forceinline__ void put(const CUtensorMap& map, const Mx4GemmArgs& a, const Tile& t, int warp, int lane, int c,
+                                        const float (&x)[32])
+    {
+        const bool wide = a.dtype == kF32;
+        uint8_t* buf = base + (used & 1) * 4096;
+        const int at = c & 32 ? 4 : 0;        // first 16-byte chunk of a 16-bit row
+        if (!pending) {
+            // the buffer's store of two before has been read
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+            __syncwarp();
+        }
+        uint8_t* row = buf + lane * 128;
+        const int sw = lane & 7;
+        if (wide) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                *reinterpret_cast<float4*>(row + ((k ^ sw) << 4)) = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                uint4 v;
+                if (a.dtype == kF16)
+                    v = make_uint4(pack_out<kF16>(x[8 * k], x[8 * k + 1]), pack_out<kF16>(x[8 * k + 2], x[8 * k + 3]),
+                                   pack_out<kF16>(x[8 * k + 4], x[8 * k + 5]), pack_out<kF16>(x[8 * k + 6], x[8 * k + 7]));
+                else
+                    v = make_uint4(pack_out<kBF16>(x[8 * k], x[8 * k + 1]), pack_out<kBF16>(x[8 * k + 2], x[8 * k + 3]),
+                                   pack_out<kBF16>(x[8 * k + 4], x[8 * k + 5]), pack_out<kBF16>(x[8 * k + 6], x[8 * k + 7]));
+                *reinterpret_cast<uint4*>(row + (((at + k) ^ sw) << 4)) = v;
+            }
+            pending = !pending;
+            if (pending) return;
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        const int col = t.d_col + (wide ? c : c & ~32);
+        if (lane == 0) {
+            if (col < a.d_cols) tma_store_2d(&map, col, static_cast<int>(t.d_row) + (warp & 3) * 32, smem_u32(buf));
+            else asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+        ++used;
+    }
+    __device__ __forceinline__ void done(int lane)
+    {
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    }
+};
+
 // ---------------------------------------------------------------------------
 // The kernel.  Cluster of a.split CTAs along the contraction (1: none, and
 // each CTA walks tiles blockIdx.x, + gridDim.x, ...; else each cluster has
-// one tile).
+// one tile).  PAIR: two CTAs work on one tile of 256 x BN with the MMA that
+// spans both (cta_group::2).  Each holds its 128 rows of P and half of Q's
+// rows, so a tile's operands are read once by the pair: a third less traffic
+// from L2 per product, which bounds the main loop.  The first CTA issues the
+// MMAs; loads, scales and the epilogue run in both.
 // ---------------------------------------------------------------------------
-template <int BN, bool SWAP>
+template <int BN, bool SWAP, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
 mx4_gemm_kernel(const __grid_constant__ Mx4GemmMaps maps, const Mx4GemmArgs a)
 {
-    using G = Geo<BN>;
+    using G = Geo<BN, SWAP, PAIR>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ int32_t start[kMaxGroups + 1], first[kMaxGroups + 1];
-    __shared__ __align__(8) uint64_t bars[3 * G::kStages + 5];
+    __shared__ __align__(8) uint64_t bars[4 * G::kStages + 5];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t{1023});
-    uint8_t* sf_smem = smem + G::kStages * G::kStageCodes;
+    uint8_t* out_smem = smem + G::kStages * G::kStageCodes;          // 1,024-byte aligned store buffers
+    uint8_t* sf_smem = out_smem + G::kOutBytes;
     const uint32_t codes_at = smem_u32(smem), sf_at = smem_u32(sf_smem), bar0 = smem_u32(bars);
     auto full = [&](int s) { return bar0 + 8u * s; };
     auto empty = [&](int s) { return bar0 + 8u * (G::kStages + s); };
     auto sf_full = [&](int s) { return bar0 + 8u * (2 * G::kStages + s); };
-    auto acc_full = [&](int b) { return bar0 + 8u * (3 * G::kStages + b); };
-    auto acc_empty = [&](int b) { return bar0 + 8u * (3 * G::kStages + 2 + b); };
-    const uint32_t drain = bar0 + 8u * (3 * G::kStages + 4);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // where a stage's scales land: on their own in a pair, whose codes all land on the first CTA's `full`
+    auto sf_land = [&](int s) { return bar0 + 8u * (PAIR ? 3 * G::kStages + s : s); };
+    auto acc_full = [&](int b) { return bar0 + 8u * (4 * G::kStages + b); };
+    auto acc_empty = [&](int b) { return bar0 + 8u * (4 * G::kStages + 2 + b); };
+    const uint32_t drain = bar0 + 8u * (4 * G::kStages + 4);
+    const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
+    const int split = a.split;
+    int rank = 0;
+    if (PAIR || split > 1) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    const int half = PAIR ? rank : 0, ctas = PAIR ? 2 : split;
+    // arrives at the first CTA's barrier
+    auto arrive_first = [&](uint32_t bar) {
+        if (PAIR) bar_arrive_cluster(in_rank(bar, 0));
+        else bar_arrive(bar);
+    };
 
     if (tid == 0) {
         for (int s = 0; s < G::kStages; ++s) {
             bar_init(full(s), 1);
             bar_init(empty(s), 1);
-            bar_init(sf_full(s), 4);
+            bar_init(sf_full(s), PAIR ? 2 : 1);
+            if (PAIR) bar_init(sf_land(s), 1);
         }
         for (int b = 0; b < 2; ++b) {
             bar_init(acc_full(b), 1);
-            bar_init(acc_empty(b), 4);
+            bar_init(acc_empty(b), PAIR ? 8 : 4);
         }
         bar_init(drain, 1);
         abort_flag = 0;
@@ -372,30 +504,35 @@ mx4_gemm_kernel(const __grid_constant__ Mx4GemmMaps maps, const Mx4GemmArgs a)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     if (warp == 2) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
-                     :: "r"(smem_u32(&tmem_slot)), "r"(G::kTmemCols) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        if (PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                         :: "r"(smem_u32(&tmem_slot)), "r"(G::kTmemCols) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                         :: "r"(smem_u32(&tmem_slot)), "r"(G::kTmemCols) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        }
     }
     if (a.offsets) {
+        constexpr int kX = SWAP ? BN : (PAIR ? 2 * kPRows : kPRows);
         if (a.ragged_k) ragged_table(a.offsets, a.groups, a.x_rows, 128, 1, start, first, tid, kThreads);
-        else ragged_table(a.offsets, a.groups, a.x_rows, SWAP ? BN : kPRows, a.w_tiles, start, first, tid, kThreads);
+        else ragged_table(a.offsets, a.groups, a.x_rows, kX, a.w_tiles, start, first, tid, kThreads);
     }
     fence_before();
     __syncthreads();
+    if (PAIR) cluster_sync();            // the barriers exist before the other CTA's loads and arrivals reach them
     fence_after();
     const uint32_t tmem = tmem_slot;
 
-    const int split = a.split;
-    int rank = 0;
-    if (split > 1) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     const int tiles = (a.offsets && !a.ragged_k) ? first[a.groups] : a.tiles;
-    const int t0 = blockIdx.x / split, dt = gridDim.x / split;
+    const int t0 = blockIdx.x / ctas, dt = gridDim.x / ctas;
 
     // the 64-element steps [k_lo, k_hi) of a tile that this CTA sums: whole stages, evenly over the ranks
     auto k_range = [&](const Tile& t, int* lo, int* hi) {
-        const int stages = (t.k64 + 3) / 4;
-        *lo = min(t.k64, stages * rank / split * 4);
-        *hi = min(t.k64, stages * (rank + 1) / split * 4);
+        const int stages = (t.k64 + 3) / 4, part = PAIR ? 0 : rank;
+        *lo = min(t.k64, stages * part / split * 4);
+        *hi = min(t.k64, stages * (part + 1) / split * 4);
     };
 
     if (warp == 0) {
@@ -403,7 +540,7 @@ mx4_gemm_kernel(const __grid_constant__ Mx4GemmMaps maps, const Mx4GemmArgs a)
             uint32_t it = 0;
             bool ok = true;
             for (int t = t0; t < tiles && ok; t += dt) {
-                const Tile o = tile_at<BN, SWAP>(a, start, first, t);
+                const Tile o = tile_at<BN, SWAP, PAIR>(a, start, first, t, half);
                 int lo, hi;
                 k_range(o, &lo, &hi);
                 const int px = o.p_sf & ~3, qx = o.q_sf & ~3;
@@ -412,63 +549,103 @@ mx4_gemm_kernel(const __grid_constant__ Mx4GemmMaps maps, const Mx4GemmArgs a)
                     if (it >= G::kStages && !(ok = bar_wait(empty(s), (it / G::kStages - 1) & 1, &abort_flag))) break;
                     const uint32_t c = codes_at + s * G::kStageCodes, f = sf_at + s * G::kStageScales;
                     const int kg = o.kg0 + k / 2;
-                    bar_expect(full(s), G::kTx);
-                    tma_2d(c, &maps.p_codes, kg * 64, o.p_row, full(s));
-                    tma_2d(c + G::kCodesP, &maps.q_codes, kg * 64, o.q_row, full(s));
-                    tma_2d(f, &maps.p_scales, px, kg, full(s));
-                    tma_2d(f + G::kScalesQAt, &maps.q_scales, qx, kg, full(s));
+                    uint32_t land = full(s);
+                    if (PAIR) {
+                        bar_expect(sf_land(s), G::kTxScales);
+                        if (rank == 0) bar_expect(full(s), 2 * G::kTxCodes);
+                        land = in_rank(full(s), 0);
+                    } else {
+                        bar_expect(full(s), G::kTxCodes + G::kTxScales);
+                    }
+                    tma_2d<PAIR>(c, &maps.p_codes, kg * 64, o.p_row, land);
+                    tma_2d<PAIR>(c + G::kCodesP, &maps.q_codes, kg * 64, o.q_row, land);
+                    tma_2d(f, &maps.p_scales, px, kg, sf_land(s));
+                    tma_2d(f + G::kScalesQAt, &maps.q_scales, qx, kg, sf_land(s));
                 }
             }
-            if (abort_flag)      // let the copies in flight land before the CTA's memory goes away
-                for (int s = 0; s < G::kStages; ++s) {
-                    const uint32_t uses = it > static_cast<uint32_t>(s) ? (it - s - 1) / G::kStages + 1 : 0;
-                    for (uint32_t i = 0; uses > 0 && i < kWaitLimit && !bar_try(full(s), (uses - 1) & 1); ++i) {}
+            // every stage's last use is over before the CTA's memory goes
+            // away: its copies have landed and its commits have arrived (the
+            // wait stays bounded; after an abort it looks at the copies only)
+            for (int s = 0; s < G::kStages; ++s) {
+                const uint32_t uses = it > static_cast<uint32_t>(s) ? (it - s - 1) / G::kStages + 1 : 0;
+                if (uses == 0) continue;
+                if (ok && !abort_flag) {
+                    bar_wait(empty(s), (uses - 1) & 1, &abort_flag);
+                } else {
+                    for (uint32_t i = 0; i < kWaitLimit && !bar_try(sf_land(s), (uses - 1) & 1); ++i) {}
+                    if (PAIR && rank == 0) for (uint32_t i = 0; i < kWaitLimit && !bar_try(full(s), (uses - 1) & 1); ++i) {}
                 }
+            }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            // kind::mxf4: E2M1 operands (1), E8M0 scales, M = 128, N = BN
-            constexpr uint32_t kIdesc = 1u << 7 | 1u << 10 | static_cast<uint32_t>(BN >> 3) << 17 | 1u << 23 | 1u << 27;
-            uint32_t it = 0, n = 0;
+        if (half == 0) {
+            // The whole warp runs the loop and one elected lane issues, so
+            // that the compiler sees uniform control flow and keeps the
+            // descriptors in uniform registers: issued by a single lane's own
+            // branch, a stage took 1,300 cycles to issue and 512 to compute.
+            // kind::mxf4: E2M1 operands (1), E8M0 scales, M = 128 (pair: 256), N = BN
+            constexpr uint32_t kIdesc = 1u << 7 | 1u << 10 | static_cast<uint32_t>(BN >> 3) << 17 | 1u << 23 | (PAIR ? 2u : 1u) << 27;
+            uint32_t n = 0, s = 0, ph = 0, slot = 0;
+            uint32_t es = 0, eph = 0, ahead = 0;         // the stage kSfSlots before, and how many stages were issued (up to kSfSlots)
             bool ok = true;
             for (int t = t0; t < tiles && ok; t += dt) {
-                const Tile o = tile_at<BN, SWAP>(a, start, first, t);
+                const Tile o = tile_at<BN, SWAP, PAIR>(a, start, first, t, half);
                 int lo, hi;
                 k_range(o, &lo, &hi);
-                if (lo >= hi) continue;                  // nothing to sum: the epilogue takes zeros
-                const int b = n & 1;
+                const int steps = __shfl_sync(0xFFFFFFFFu, hi - lo, 0);
+                if (steps <= 0) continue;                // nothing to sum: the epilogue takes zeros
+                const uint32_t b = n & 1;
                 if (n >= G::kAccLag) {
                     const uint32_t m = n - G::kAccLag;
-                    if (!(ok = bar_wait(acc_empty(m & 1), (m >> 1) & 1, &abort_flag))) break;
+                    if (!(ok = warp_wait(acc_empty(m & 1), (m >> 1) & 1, &abort_flag))) break;
                 }
-                fence_after();
                 const uint32_t d = tmem + b * G::kAccStep;
-                for (int k = lo; k < hi; k += 4, ++it) {
-                    const int s = it % G::kStages;
-                    const uint32_t ph = (it / G::kStages) & 1;
-                    if (!(ok = bar_wait(full(s), ph, &abort_flag))) break;
-                    if (!(ok = bar_wait(sf_full(s), ph, &abort_flag))) break;
-                    fence_after();
-                    const uint32_t c = codes_at + s * G::kStageCodes;
-                    const uint64_t pd = tile_desc(c), qd = tile_desc(c + G::kCodesP);
-                    const uint32_t sf = tmem + G::kSfBase + s * G::kSfCols;
-                    const int steps = min(4, hi - k);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if (j >= steps) break;
-                        const uint32_t id = 2u * (j & 1);
-                        mma_mx4(d, pd + 2 * j, qd + 2 * j, kIdesc | id << 4 | id << 29, sf + 4 * (j >> 1),
-                                sf + 8 + G::kQCols * (j >> 1), k > lo || j > 0);
+                for (int k = 0; k < steps; k += 4) {
+                    if (!(ok = warp_wait(full(s), ph, &abort_flag))) break;
+                    if (!(ok = warp_wait(sf_full(s), ph, &abort_flag))) break;
+                    if constexpr (G::kSfSlots < G::kStages) {
+                        // the slot's last readers: the MMAs of kSfSlots stages before
+                        if (ahead < G::kSfSlots) {
+                            ++ahead;
+                        } else {
+                            if (!(ok = warp_wait(empty(es), eph, &abort_flag))) break;
+                            if (++es == G::kStages) { es = 0; eph ^= 1; }
+                        }
                     }
-                    mma_commit(empty(s));
+                    fence_after();
+                    const uint32_t c = codes_at + s * G::kStageCodes, sf_from = sf_at + s * G::kStageScales;
+                    const uint32_t sf = tmem + G::kSfBase + slot * G::kSfCols;
+                    const uint64_t pd = tile_desc(c), qd = tile_desc(c + G::kCodesP);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            copy_scales<PAIR>(sf + 4 * g, sf_from + 512 * g);
+#pragma unroll
+                            for (int q = 0; q < G::kQAtoms; ++q)
+                                copy_scales<PAIR>(sf + 8 + G::kQCols * g + 4 * q, sf_from + G::kScalesQAt + 512 * (G::kQAtoms * g + q));
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            if (k + j >= steps) break;
+                            const uint32_t id = 2u * (j & 1);
+                            mma_mx4<PAIR>(d, pd + 2 * j, qd + 2 * j, kIdesc | id << 4 | id << 29, sf + 4 * (j >> 1),
+                                          sf + 8 + G::kQCols * (j >> 1), k + j > 0);
+                        }
+                        mma_commit<PAIR>(empty(s));
+                        if (k + 4 >= steps) mma_commit<PAIR>(acc_full(b));
+                    }
+                    __syncwarp();
+                    if (++s == G::kStages) { s = 0; ph ^= 1; }
+                    if (++slot == G::kSfSlots) slot = 0;
                 }
-                if (!ok) break;
-                mma_commit(acc_full(b));
                 ++n;
             }
             if (abort_flag) {
-                mma_commit(drain);
-                for (uint32_t i = 0; i < kWaitLimit && !bar_try(drain, 0); ++i) {}
+                if (elect_one()) {
+                    mma_commit<PAIR>(drain);
+                    for (uint32_t i = 0; i < kWaitLimit && !bar_try(drain, 0); ++i) {}
+                }
+                __syncwarp();
             }
         }
     } else if (warp == 3) {
@@ -483,48 +660,61 @@ mx4_gemm_kernel(const __grid_constant__ Mx4GemmMaps maps, const Mx4GemmArgs a)
             }
         }
     } else if (warp >= 4 && warp < 8) {
-        const uint32_t quad = static_cast<uint32_t>(warp & 3) << 21;     // lane field: 32 * quadrant << 16
+        // Scales of every fourth stage: from rows in order to the order that
+        // copy_scales takes (row 32 j + r at word [r][j]), in place.
         uint32_t it = 0;
         bool ok = true;
         for (int t = t0; t < tiles && ok; t += dt) {
-            const Tile o = tile_at<BN, SWAP>(a, start, first, t);
+            const Tile o = tile_at<BN, SWAP, PAIR>(a, start, first, t, half);
             int lo, hi;
             k_range(o, &lo, &hi);
             const int pr = o.p_sf & 3, qr = o.q_sf & 3;
             for (int k = lo; k < hi; k += 4, ++it) {
+                if ((it & 3) != (warp & 3u)) continue;
                 const int s = it % G::kStages;
-                if (!(ok = warp_wait(full(s), (it / G::kStages) & 1, &abort_flag))) break;
-                const uint32_t* ps = reinterpret_cast<const uint32_t*>(sf_smem + s * G::kStageScales) + pr;
-                const uint32_t* qs = reinterpret_cast<const uint32_t*>(sf_smem + s * G::kStageScales + G::kScalesQAt) + qr;
-                const uint32_t at = tmem + quad + G::kSfBase + s * G::kSfCols;
+                // This warp has not seen the stage's use before, whose landing
+                // another warp waited for, and a parity only tells two
+                // neighbouring uses apart: first wait until that use is over.
+                // (The use before that one is over: the loads of it - 4, which
+                // this warp saw land, were issued after those of it - 5, which
+                // waited for it.)
+                if (it >= G::kStages && !(ok = warp_wait(empty(s), (it / G::kStages - 1) & 1, &abort_flag))) break;
+                if (!(ok = warp_wait(sf_land(s), (it / G::kStages) & 1, &abort_flag))) break;
+                uint32_t* ps = reinterpret_cast<uint32_t*>(sf_smem + s * G::kStageScales);
+                uint32_t* qs = ps + G::kScalesQAt / 4;
+                uint32_t p[2][4], q[2][G::kQAtoms][4];
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        p[g][j] = ps[g * G::kSfP + pr + 32 * j + lane];
+#pragma unroll
+                        for (int n = 0; n < G::kQAtoms; ++n) {
+                            const int r = 128 * n + 32 * j + lane;
+                            q[g][n][j] = BN >= 128 || r < BN ? qs[g * G::kSfQ + qr + r] : 0u;
+                        }
+                    }
+                __syncwarp();
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
-                    const uint32_t* p = ps + g * G::kSfP;
-                    tmem_st4(at + 4 * g, p[lane], p[32 + lane], p[64 + lane], p[96 + lane]);
-                    const uint32_t* q = qs + g * G::kSfQ;
+                    reinterpret_cast<uint4*>(ps)[32 * g + lane] = make_uint4(p[g][0], p[g][1], p[g][2], p[g][3]);
 #pragma unroll
-                    for (int c = 0; c < G::kQCols; c += 4) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int r = (c + j) * 32 + lane;
-                            w[j] = r < BN ? q[r] : 0u;
-                        }
-                        tmem_st4(at + 8 + g * G::kQCols + c, w[0], w[1], w[2], w[3]);
-                    }
+                    for (int n = 0; n < G::kQAtoms; ++n)
+                        reinterpret_cast<uint4*>(qs)[32 * (G::kQAtoms * g + n) + lane] =
+                            make_uint4(q[g][n][0], q[g][n][1], q[g][n][2], q[g][n][3]);
                 }
-                tmem_st_wait();
-                fence_before();
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) bar_arrive(sf_full(s));
+                if (lane == 0) arrive_first(sf_full(s));
             }
         }
     } else if (warp >= 8) {
         const int lane_row = (warp & 3) * 32 + lane;
         const uint32_t quad = static_cast<uint32_t>(warp & 3) << 21;
+        StoreBuffers out(out_smem + (warp & 3) * 8192);
         uint32_t n = 0;
         for (int t = t0; t < tiles; t += dt) {
-            const Tile o = tile_at<BN, SWAP>(a, start, first, t);
+            const Tile o = tile_at<BN, SWAP, PAIR>(a, start, first, t, half);
             int lo, hi;
             k_range(o, &lo, &hi);
             if (lo < hi) {
@@ -534,29 +724,44 @@ mx4_gemm_kernel(const __grid_constant__ Mx4GemmMaps maps, const Mx4GemmArgs a)
                 if (split == 1) {
                     const uint32_t acc = tmem + quad + b * G::kAccStep;
                     constexpr int kChunk = BN < 32 ? 16 : 32, kFirst = G::kOverlap / 32;
-                    // the shared columns first: the last ones of accumulator 0, the first ones of 1
-                    const int c0 = b == 0 ? BN - G::kOverlap : 0;
+                    // The shared columns first: the last ones of accumulator 0, the first ones of 1.
+                    // Chunks that share a 64-column store buffer stay neighbours.
+                    auto chunk = [&](int i) {
+                        if constexpr (kFirst == 0) return kChunk * i;
+                        else return 32 * (b ? i : (i < 2 ? 6 + i : (i < 4 ? 7 - i : i - 4)));
+                    };
+                    static_assert(kFirst == 0 || kFirst == 3, "the order above");
+                    const bool whole = !SWAP && a.tma_store && o.d_rows - (warp & 3) * 32 >= 32;
                     if constexpr (kFirst > 0) {
                         float x[kFirst][32];
 #pragma unroll
-                        for (int i = 0; i < kFirst; ++i) tmem_ld(acc + c0 + 32 * i, x[i]);
+                        for (int i = 0; i < kFirst; ++i) tmem_ld(acc + chunk(i), x[i]);
                         fence_before();
                         __syncwarp();
-                        if (lane == 0) bar_arrive(acc_empty(b));
+                        if (lane == 0) arrive_first(acc_empty(b));
 #pragma unroll
-                        for (int i = 0; i < kFirst; ++i) store_any<32, SWAP>(a, o, lane_row, c0 + 32 * i, x[i]);
+                        for (int i = 0; i < kFirst; ++i) {
+                            if (whole) out.put(maps.d, a, o, warp, lane, chunk(i), x[i]);
+                            else store_any<32, SWAP>(a, o, lane_row, chunk(i), x[i]);
+                        }
                     }
 #pragma unroll 1
                     for (int i = kFirst; i < BN / kChunk; ++i) {
-                        const int c = (c0 + kChunk * i) % BN;
+                        const int c = chunk(i);
                         float x[kChunk];
                         tmem_ld(acc + c, x);
+                        if constexpr (kChunk == 32) {
+                            if (whole) {
+                                out.put(maps.d, a, o, warp, lane, c, x);
+                                continue;
+                            }
+                        }
                         store_any<kChunk, SWAP>(a, o, lane_row, c, x);
                     }
                     if constexpr (kFirst == 0) {
                         fence_before();
                         __syncwarp();
-                        if (lane == 0) bar_arrive(acc_empty(b));
+                        if (lane == 0) arrive_first(acc_empty(b));
                     }
                 }
                 ++n;
@@ -566,6 +771,7 @@ mx4_gemm_kernel(const __grid_constant__ Mx4GemmMaps maps, const Mx4GemmArgs a)
                 for (int c = 0; c < BN; c += 16) store_any<16, SWAP>(a, o, lane_row, c, zero);
             }
         }
+        out.done(lane);
     }
 
     if (split > 1) {
@@ -581,7 +787,7 @@ mx4_gemm_kernel(const __grid_constant__ Mx4GemmMaps maps, const Mx4GemmArgs a)
         Tile o{};
         int lo = 0, hi = 0, quads = 0;
         if (mine) {
-            o = tile_at<BN, SWAP>(a, start, first, t0);
+            o = tile_at<BN, SWAP, PAIR>(a, start, first, t0, half);
             k_range(o, &lo, &hi);
             quads = (min(BN, o.d_rows) + 3) / 4;
         }
@@ -625,8 +831,11 @@ mx4_gemm_kernel(const __grid_constant__ Mx4GemmMaps maps, const Mx4GemmArgs a)
     }
     fence_before();
     __syncthreads();
-    if (warp == 2)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(G::kTmemCols));
+    if (PAIR) cluster_sync();            // nothing of the other CTA reaches for this one's memory any more
+    if (warp == 2) {
+        if (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(G::kTmemCols));
+        else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(G::kTmemCols));
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -675,23 +884,39 @@ cudaError_t scales_map(EncodeTiled enc, CUtensorMap* m, const uint8_t* base, int
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int BN, bool SWAP>
+// D, for stores of 32 rows x 128 bytes.
+cudaError_t out_map(EncodeTiled enc, CUtensorMap* m, const Mx4GemmArgs& a)
+{
+    const int es = elem_bytes(a.dtype);
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(a.d_cols), static_cast<cuuint64_t>(a.d_rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(a.ldd) * es};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / es), 32}, ones[2] = {1, 1};
+    const CUtensorMapDataType type = a.dtype == kF32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                     : a.dtype == kF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const CUresult r = enc(m, type, 2, a.d, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int BN, bool SWAP, bool PAIR>
 cudaError_t launch_as(Mx4GemmArgs a, const Mx4GemmOperands& op, int sms, cudaStream_t stream)
 {
-    using G = Geo<BN>;
+    using G = Geo<BN, SWAP, PAIR>;
     EncodeTiled enc = nullptr;
     cudaError_t e = encoder(&enc);
     if (e != cudaSuccess) return e;
     const Mx4Operand& p = SWAP ? op.w : op.x;
     const Mx4Operand& q = SWAP ? op.x : op.w;
-    Mx4GemmMaps maps;
+    Mx4GemmMaps maps{};
     if ((e = codes_map(enc, &maps.p_codes, p.codes, p.code_rows, p.pitch, kPRows)) != cudaSuccess) return e;
-    if ((e = codes_map(enc, &maps.q_codes, q.codes, q.code_rows, q.pitch, BN)) != cudaSuccess) return e;
+    if ((e = codes_map(enc, &maps.q_codes, q.codes, q.code_rows, q.pitch, G::kQRows)) != cudaSuccess) return e;
     if ((e = scales_map(enc, &maps.p_scales, p.scales, p.scale_rows, p.pitch / 64, G::kSfP)) != cudaSuccess) return e;
     if ((e = scales_map(enc, &maps.q_scales, q.scales, q.scale_rows, q.pitch / 64, G::kSfQ)) != cudaSuccess) return e;
-    constexpr int kX = SWAP ? BN : kPRows, kW = SWAP ? kPRows : BN;
+    a.tma_store = !SWAP && a.vec && !a.accumulate;
+    if (a.tma_store && (e = out_map(enc, &maps.d, a)) != cudaSuccess) return e;
+    constexpr int kP = PAIR ? 2 * kPRows : kPRows, kX = SWAP ? BN : kP, kW = SWAP ? kPRows : BN;
     a.w_tiles = static_cast<int>((a.w_rows + kW - 1) / kW);
-    a.p_tiles = static_cast<int>((a.p_rows + kPRows - 1) / kPRows);
+    a.p_tiles = static_cast<int>((a.p_rows + kP - 1) / kP);
     a.q_tiles = a.w_tiles;
     int64_t tiles;                      // exact, or (groups of rows) at most
     if (a.ragged_k) tiles = static_cast<int64_t>(a.groups) * a.p_tiles * a.q_tiles;
@@ -699,8 +924,10 @@ cudaError_t launch_as(Mx4GemmArgs a, const Mx4GemmOperands& op, int sms, cudaStr
     if (tiles > INT32_MAX / 8) return cudaErrorInvalidConfiguration;
     a.tiles = static_cast<int>(tiles);
     if (tiles == 0) return cudaSuccess;
-    const int64_t ctas = a.split > 1 ? tiles * a.split : std::min<int64_t>(tiles, sms * (512 / G::kTmemCols > 1 && G::kSmem < 110000 ? 2 : 1));
-    auto* k = mx4_gemm_kernel<BN, SWAP>;
+    constexpr int kResident = G::kTmemCols <= 256 && G::kSmem < 104000 ? 2 : 1;      // CTAs an SM holds
+    const int cluster = PAIR ? 2 : a.split;
+    const int64_t ctas = a.split > 1 ? tiles * cluster : std::min<int64_t>(tiles, sms / cluster * kResident) * cluster;
+    auto* k = mx4_gemm_kernel<BN, SWAP, PAIR>;
     if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem)) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas));
@@ -709,7 +936,7 @@ cudaError_t launch_as(Mx4GemmArgs a, const Mx4GemmOperands& op, int sms, cudaStr
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(a.split);
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -726,7 +953,8 @@ cudaError_t launch_mx4_gemm(Mx4GemmArgs a, const Mx4GemmOperands& op, cudaStream
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     a.split = 1;
-    if (a.ragged_k) return launch_as<128, false>(a, op, sms, stream);
+    if (a.ragged_k) return a.p_rows > 128 && a.w_rows > 128 ? launch_as<256, false, true>(a, op, sms, stream)
+                                                            : launch_as<128, false, false>(a, op, sms, stream);
     // Few token rows a group: the weights take the 128-row side of the tile,
     // the tokens its narrow side, and the contraction is cut over a cluster
     // so that the weights' tiles reach every SM.
@@ -737,12 +965,12 @@ cudaError_t launch_mx4_gemm(Mx4GemmArgs a, const Mx4GemmOperands& op, cudaStream
         const int64_t xt = (a.x_rows + bn - 1) / bn + (a.offsets ? std::min<int64_t>(a.groups, a.x_rows) : 0);
         const int stages = (a.k64 + 3) / 4, most = bn == 16 ? 8 : 4;
         while (a.split < most && a.split * 2 <= stages && wt * xt * a.split * 2 <= sms) a.split *= 2;
-        if (bn == 16) return launch_as<16, true>(a, op, sms, stream);
-        if (bn == 32) return launch_as<32, true>(a, op, sms, stream);
-        return launch_as<64, true>(a, op, sms, stream);
+        if (bn == 16) return launch_as<16, true, false>(a, op, sms, stream);
+        if (bn == 32) return launch_as<32, true, false>(a, op, sms, stream);
+        return launch_as<64, true, false>(a, op, sms, stream);
     }
-    if (a.w_rows > 128) return launch_as<256, false>(a, op, sms, stream);
-    return launch_as<128, false>(a, op, sms, stream);
+    if (mean > 128 && a.w_rows > 128) return launch_as<256, false, true>(a, op, sms, stream);
+    return launch_as<128, false, false>(a, op, sms, stream);
 }
 
 cudaError_t mx4_error_count(unsigned int* out) { return cudaMemcpyFromSymbol(out, g_mx4_errors, sizeof(*out)); }
