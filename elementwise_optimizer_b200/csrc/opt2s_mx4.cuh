@@ -63,20 +63,39 @@ __device__ __forceinline__ uint32_t encode8(float x0, float x1, float x2, float 
     return r;
 }
 
-// One E2M1 code rounded stochastically with the byte r: the upper of the two
-// neighbouring codes when |x| lies more than (r + 0.5)/256 of the way to it.
-// From 1 on a code is the exponent and one mantissa bit, the way is the other
-// 22 bits, and the comparison is the carry of an addition; below 1 the same
-// holds for 1 + |x|.  That sum is rounded up, which cannot move the way past
-// a threshold (a multiple of 2^13 units of the last bit) that it had not
-// passed, so the comparison is exact for every x.
-__device__ __forceinline__ uint32_t encode_noise(float x, uint32_t r)
+// Stochastic rounding of a scaled element with the byte r: code c or c + 1,
+// the upper one when |x| lies more than (r + 0.5)/256 of the way from c's
+// magnitude to the next.  Returned in the top byte; `flipped` holds the
+// complements of four random bytes, `j` says which one is this element's.
+//
+// With a = min(|x|, 6), y = a + max(a, 1) is 1 + a below 1 and 2 a from there
+// on: its exponent and first mantissa bit count the codes, and the other 22
+// bits are the way to the next.  Shifted left by two, the code (plus 254)
+// fills the top byte and the way the 24 bits under it, and the comparison is
+// the carry of adding 2^24 - 1 - 256^2 r - 2^15.  The sum 1 + a is rounded up,
+// which cannot take the way past a threshold (a multiple of 2^13 units of the
+// last bit) that it had not passed, so the comparison is exact for every x.
+__device__ __forceinline__ uint32_t noise_code(float x, uint32_t flipped, int j)
 {
     const float a = fminf(fabsf(x), 6.0f);
-    const bool small = a < 1.0f;
-    const uint32_t y = __float_as_uint(small ? __fadd_ru(a, 1.0f) : a);
-    const uint32_t code = ((y + (0x3FDFFFu - (r << 14))) >> 22) - (small ? 254u : 252u);
-    return code | (__float_as_uint(x) >> 31 << 3);
+    const float y = __fadd_ru(a, fmaxf(a, 1.0f));
+    const uint32_t add = __byte_perm(flipped, 0x00027FFFu, 0x6054u | static_cast<uint32_t>(j) << 8);
+    return (__float_as_uint(y) << 2) + add;
+}
+
+// The top bytes of four words as one word.
+__device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
+}
+
+// Eight codes in a word from noise_code's results for x[0..7], signs added.
+__device__ __forceinline__ uint32_t pack_noise(const uint32_t (&t)[8], const float (&x)[8])
+{
+    const uint32_t even = top_bytes(t[0], t[2], t[4], t[6]), odd = top_bytes(t[1], t[3], t[5], t[7]);
+    const uint32_t se = top_bytes(__float_as_uint(x[0]), __float_as_uint(x[2]), __float_as_uint(x[4]), __float_as_uint(x[6]));
+    const uint32_t so = top_bytes(__float_as_uint(x[1]), __float_as_uint(x[3]), __float_as_uint(x[5]), __float_as_uint(x[7]));
+    return even + (odd << 4) | (se & 0x80808080u) >> 4 | (so & 0x80808080u);
 }
 
 // The two values of a byte of codes.
@@ -124,28 +143,24 @@ template <> struct Src<kF16> {
 // The largest magnitude of words of a 16-bit type, each half on its own.
 __device__ __forceinline__ uint32_t amax_halves(uint32_t amax, uint32_t w) { return __vmaxu2(amax, w & 0x7FFF7FFFu); }
 
-// The 16 bytes of codes of a block: get(i) is element i, noise(i) its random
-// byte, `scale` the block's scale byte.
-template <bool NOISE, typename Get, typename Noise>
-__device__ __forceinline__ uint4 encode_block(uint32_t scale, Get get, Noise noise)
+// One word of a block's codes: eight elements x times 2^-e.  flipped(i) and
+// at(i) give element i's random byte as noise_code takes it.
+template <bool NOISE, typename Get, typename Flipped, typename At>
+__device__ __forceinline__ uint32_t encode_word(uint32_t scale, float inv, Get get, Flipped flipped, At at)
 {
-    const float inv = inverse_scale(scale);
-    uint32_t w[4];
+    float x[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        float x[8];
+    for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(get(i), inv);
+    uint32_t w;
+    if (NOISE) {
+        uint32_t t[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(get(8 * k + i), inv);
-        if (NOISE) {
-            w[k] = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[k] |= encode_noise(x[i], noise(8 * k + i)) << (4 * i);
-        } else {
-            w[k] = encode8(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]);
-        }
-        if (scale == 255u) w[k] = 0;                 // a NaN block's codes
+        for (int i = 0; i < 8; ++i) t[i] = noise_code(x[i], flipped(i), at(i));
+        w = pack_noise(t, x);
+    } else {
+        w = encode8(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]);
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    return scale == 255u ? 0u : w;               // a NaN block's codes are 0
 }
 
 // ---------------------------------------------------------------------------
@@ -209,17 +224,23 @@ __device__ __forceinline__ void tile_rows_out(const uint8_t* tile, const uint8_t
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 const uint4 v = *reinterpret_cast<const uint4*>(noise + noise_chunk<TC>(r, blk * 2 + c));
-                nz[4 * c] = v.x; nz[4 * c + 1] = v.y; nz[4 * c + 2] = v.z; nz[4 * c + 3] = v.w;
+                nz[4 * c] = ~v.x; nz[4 * c + 1] = ~v.y; nz[4 * c + 2] = ~v.z; nz[4 * c + 3] = ~v.w;
             }
         }
 #pragma unroll
         for (int i = 0; i < 4 * C; ++i) amax = S::kBytes == 2 ? amax_halves(amax, w[i]) : max(amax, w[i] & 0x7FFFFFFFu);
         if (S::kBytes == 2) amax = S::magnitude(max(amax & 0xFFFFu, amax >> 16));
         const uint32_t s = scale_byte(amax);
-        const uint4 codes = encode_block<NOISE>(
-            s, [&](int i) { return S::element(w, i); }, [&](int i) { return nz[i / 4] >> (8 * (i & 3)) & 255u; });
+        const float inv = inverse_scale(s);
+        uint32_t codes[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            codes[k] = encode_word<NOISE>(
+                s, inv, [&](int i) { return S::element(w, 8 * k + i); }, [&](int i) { return nz[2 * k + i / 4]; },
+                [](int i) { return i & 3; });
         bytes |= s << (8 * b);
-        if (r < o.rows) *reinterpret_cast<uint4*>(o.codes + r * o.pitch + blk * 16) = codes;
+        if (r < o.rows)
+            *reinterpret_cast<uint4*>(o.codes + r * o.pitch + blk * 16) = make_uint4(codes[0], codes[1], codes[2], codes[3]);
     }
     uint8_t* at = o.scales + 4 * r + part * B;
     if (B == 4) *reinterpret_cast<uint32_t*>(at) = bytes;
@@ -237,32 +258,42 @@ __device__ __forceinline__ void tile_cols_out(const uint8_t* tile, const uint8_t
     for (int t = tid; t < kTasks; t += THREADS) {
         const int c0 = (t % kAcross) * W, rb = t / kAcross;
         if (c0 >= o.scale_cols) continue;
-        uint32_t w[32], nz[W][8] = {}, amax = 0;
+        uint32_t w[32], amax = 0;
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-            const int r = rb * 32 + i;
-            w[i] = *reinterpret_cast<const uint32_t*>(tile + tile_chunk<DT, TC>(r, c0 / P) + (c0 % P) * S::kBytes);
+            w[i] = *reinterpret_cast<const uint32_t*>(tile + tile_chunk<DT, TC>(rb * 32 + i, c0 / P) + (c0 % P) * S::kBytes);
             amax = W == 2 ? amax_halves(amax, w[i]) : max(amax, w[i] & 0x7FFFFFFFu);
+        }
+        uint32_t s[W], codes[W][4];
+        float inv[W];
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            s[j] = scale_byte(W == 2 ? S::magnitude(j ? amax >> 16 : amax & 0xFFFFu) : amax);
+            inv[j] = inverse_scale(s[j]);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            uint32_t nz[8] = {};
             if (NOISE) {
-                const uint8_t* np = noise + noise_chunk<TC>(r, c0 / 16) + c0 % 16;
-                if (W == 2) {
-                    const uint32_t n = *reinterpret_cast<const uint16_t*>(np);
-                    nz[0][i / 4] |= (n & 255u) << (8 * (i & 3));
-                    nz[W - 1][i / 4] |= (n >> 8) << (8 * (i & 3));
-                } else {
-                    nz[0][i / 4] |= static_cast<uint32_t>(*np) << (8 * (i & 3));
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint8_t* np = noise + noise_chunk<TC>(rb * 32 + 8 * k + i, c0 / 16) + c0 % 16;
+                    nz[i] = ~(W == 2 ? static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(np)) : static_cast<uint32_t>(*np));
                 }
             }
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+                codes[j][k] = encode_word<NOISE>(
+                    s[j], inv[j], [&](int i) { return W == 2 ? S::half(w[8 * k + i], j) : __uint_as_float(w[8 * k + i]); },
+                    [&](int i) { return nz[i]; }, [&](int) { return j; });
         }
 #pragma unroll
         for (int j = 0; j < W; ++j) {
             if (c0 + j >= o.scale_cols) break;
-            const uint32_t s = scale_byte(W == 2 ? S::magnitude(j ? amax >> 16 : amax & 0xFFFFu) : amax);
-            const uint4 codes = encode_block<NOISE>(
-                s, [&](int i) { return W == 2 ? S::half(w[i], j) : __uint_as_float(w[i]); },
-                [&](int i) { return nz[j][i / 4] >> (8 * (i & 3)) & 255u; });
-            if (c0 + j < o.cols) *reinterpret_cast<uint4*>(o.codes_t + (c0 + j) * o.pitch_t + rb * 16) = codes;
-            o.scales_t[4 * (c0 + j) + rb] = static_cast<uint8_t>(s);
+            if (c0 + j < o.cols)
+                *reinterpret_cast<uint4*>(o.codes_t + (c0 + j) * o.pitch_t + rb * 16) =
+                    make_uint4(codes[j][0], codes[j][1], codes[j][2], codes[j][3]);
+            o.scales_t[4 * (c0 + j) + rb] = static_cast<uint8_t>(s[j]);
         }
     }
 }
