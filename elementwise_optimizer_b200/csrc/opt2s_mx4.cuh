@@ -23,6 +23,14 @@
 namespace opt2s {
 namespace {
 
+// A 32-byte store to a 32-byte aligned address.
+__device__ __forceinline__ void store32(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e, uint32_t f,
+                                        uint32_t g, uint32_t h)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 :: "l"(p), "r"(a), "r"(b), "r"(c), "r"(d), "r"(e), "r"(f), "r"(g), "r"(h) : "memory");
+}
+
 // ---------------------------------------------------------------------------
 // Elements
 // ---------------------------------------------------------------------------

@@ -183,7 +183,7 @@ OPT2S_API int opt2s_mx4_dequantize(const opt2s_mx4* q, void* out, int32_t dtype,
     r[n++] = span(out, q->slabs * q->rows * q->cols * es, true);
     if ((st = opt2s::overlap_status(r, n)) != OPT2S_OK) return st;
     const opt2s::Mx4DequantArgs a{q->codes, q->scales, out, q->slabs, q->rows, q->cols,
-                                  aligned(out, 16) && q->cols % 8 == 0};
+                                  aligned(out, 32) && q->cols % 16 == 0};
     const cudaError_t e = opt2s::launch_mx4_dequantize(a, dtype, stream);
     if (e != cudaSuccess) return opt2s::record_cuda_error(e);
     opt2s::count_launches(1);

@@ -137,58 +137,89 @@ __device__ __forceinline__ float scale_value(uint32_t s)
     return s == 255u ? __uint_as_float(0x7FC00000u) : (s == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(s << 23));
 }
 
+template <int DT> __device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    if (DT == kF16) {
+        const __half2 v = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
 // grid: x = groups of 4 rows, y = 4,096-column parts, z = slabs.  A thread
-// takes 8 elements (4 bytes of codes) a step.
+// takes 16 elements (8 bytes of codes, half a block) of each row; all loads
+// come first, and 16-bit outputs are stored 32 bytes a thread.  Outputs whose
+// rows do not start on 32 bytes take two elements a thread and step instead,
+// so that a warp still stores neighbouring elements.
 template <int DT>
 __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const Mx4DequantArgs a)
 {
-    constexpr int kRows = 4, kPart = 512 * 8;         // 4 rows of 512 x 8 columns a CTA: 8 steps of 256 threads
+    constexpr int kRows = 4, kPart = 4096;
     const int64_t cp = (a.cols + 127) / 128 * 128, rp = (a.rows + 3) / 4 * 4;
     const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kRows, slab = blockIdx.z, col0 = static_cast<int64_t>(blockIdx.y) * kPart;
+    const int rows = static_cast<int>(min(static_cast<int64_t>(kRows), a.rows - row0));
+    const uint8_t* codes = a.codes + (slab * a.rows + row0) * (cp / 2);
+    const uint8_t* scales = a.scales + (slab * rp + row0) * 4;
+    const int64_t group = a.slabs * rp * 4;           // bytes of scales per 128-column group
+    const int64_t out0 = (slab * a.rows + row0) * a.cols;
+    if (a.vec) {
+        const int64_t c0 = col0 + threadIdx.x * 16;
+        if (c0 >= a.cols) return;
+        uint2 w[kRows];
+        uint32_t s[kRows];
 #pragma unroll
-    for (int it = 0; it < kRows * 2; ++it) {
-        const int64_t r = row0 + it / 2, c0 = col0 + ((it & 1) * 256 + threadIdx.x) * 8;
-        if (r >= a.rows || c0 >= a.cols) continue;
-        const int64_t row = slab * a.rows + r;
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(a.codes + row * (cp / 2) + c0 / 2);
-        const float scale = scale_value(a.scales[(((c0 >> 7) * a.slabs + slab) * rp + r) * 4 + ((c0 >> 5) & 3)]);
-        float x[8];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float2 f = decode2(w >> (8 * k) & 255u);
-            x[2 * k] = __fmul_rn(f.x, scale);
-            x[2 * k + 1] = __fmul_rn(f.y, scale);
+        for (int r = 0; r < kRows; ++r) {
+            if (r < rows) {
+                w[r] = *reinterpret_cast<const uint2*>(codes + r * (cp / 2) + c0 / 2);
+                s[r] = scales[(c0 >> 7) * group + r * 4 + ((c0 >> 5) & 3)];
+            }
         }
-        const int64_t at = row * a.cols + c0;
-        const bool vec = a.vec && c0 + 8 <= a.cols;
-        if (DT == kF32) {
-            float* d = static_cast<float*>(a.out) + at;
-            if (vec) {
-                reinterpret_cast<float4*>(d)[0] = make_float4(x[0], x[1], x[2], x[3]);
-                reinterpret_cast<float4*>(d)[1] = make_float4(x[4], x[5], x[6], x[7]);
-            } else {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) if (c0 + k < a.cols) d[k] = x[k];
+        for (int r = 0; r < kRows; ++r) {
+            if (r >= rows) break;
+            const float scale = scale_value(s[r]);
+            float x[16];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float2 f = decode2((k < 4 ? w[r].x : w[r].y) >> (8 * (k & 3)) & 255u);
+                x[2 * k] = __fmul_rn(f.x, scale);
+                x[2 * k + 1] = __fmul_rn(f.y, scale);
             }
-        } else {
-            uint32_t h[4];
+            const int64_t at = out0 + r * a.cols + c0;
+            if (DT == kF32) {
+                uint32_t* d = static_cast<uint32_t*>(a.out) + at;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (DT == kBF16) {
-                    const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
-                    h[k] = *reinterpret_cast<const uint32_t*>(&v);
-                } else {
-                    const __half2 v = __floats2half2_rn(x[2 * k], x[2 * k + 1]);
-                    h[k] = *reinterpret_cast<const uint32_t*>(&v);
-                }
-            }
-            uint16_t* d = static_cast<uint16_t*>(a.out) + at;
-            if (vec) {
-                *reinterpret_cast<uint4*>(d) = make_uint4(h[0], h[1], h[2], h[3]);
+                for (int k = 0; k < 16; k += 8)
+                    store32(d + k, __float_as_uint(x[k]), __float_as_uint(x[k + 1]), __float_as_uint(x[k + 2]),
+                            __float_as_uint(x[k + 3]), __float_as_uint(x[k + 4]), __float_as_uint(x[k + 5]),
+                            __float_as_uint(x[k + 6]), __float_as_uint(x[k + 7]));
             } else {
+                store32(static_cast<uint16_t*>(a.out) + at, pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]),
+                        pack2<DT>(x[4], x[5]), pack2<DT>(x[6], x[7]), pack2<DT>(x[8], x[9]), pack2<DT>(x[10], x[11]),
+                        pack2<DT>(x[12], x[13]), pack2<DT>(x[14], x[15]));
+            }
+        }
+        return;
+    }
+    for (int r = 0; r < rows; ++r) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (c0 + k < a.cols) d[k] = static_cast<uint16_t>(h[k / 2] >> (16 * (k & 1)));
+        for (int it = 0; it < kPart / 512; ++it) {
+            const int64_t c0 = col0 + (it * 256 + threadIdx.x) * 2;
+            if (c0 >= a.cols) break;
+            const float2 f = decode2(codes[r * (cp / 2) + c0 / 2]);
+            const float scale = scale_value(scales[(c0 >> 7) * group + r * 4 + ((c0 >> 5) & 3)]);
+            const float x0 = __fmul_rn(f.x, scale), x1 = __fmul_rn(f.y, scale);
+            const int64_t at = out0 + r * a.cols + c0;
+            if (DT == kF32) {
+                float* d = static_cast<float*>(a.out) + at;
+                d[0] = x0;
+                if (c0 + 1 < a.cols) d[1] = x1;
+            } else {
+                uint16_t* d = static_cast<uint16_t*>(a.out) + at;
+                const uint32_t h = pack2<DT>(x0, x1);
+                d[0] = static_cast<uint16_t>(h);
+                if (c0 + 1 < a.cols) d[1] = static_cast<uint16_t>(h >> 16);
             }
         }
     }
