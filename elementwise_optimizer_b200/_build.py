@@ -36,7 +36,8 @@ MARSHAL_DIR = os.path.join(PKG, "_build")
 MARSHAL_NAME = "opt2s_marshal"
 
 COMMON = ["opt2s_kernel.cu", "opt2s_kernel8.cu", "opt2s_noalloc.cu", "opt2s_api8.cpp", "opt2s_ipc.cpp",
-          "opt2s_mx4_quant.cu", "opt2s_mx4_gemm.cu", "opt2s_mx4_step.cu", "opt2s_mx4_api.cpp"]
+          "opt2s_mx4_quant.cu", "opt2s_mx4_gemm.cu", "opt2s_mx4_step.cu", "opt2s_mx4_row.cu",
+          "opt2s_mx4_api.cpp"]
 API = "opt2s_api.cpp"
 TESTING_ONLY = ["opt2s_testing.cu"]
 SOURCES = [os.path.join(CSRC, f) for f in COMMON + [API] + TESTING_ONLY]

@@ -179,6 +179,9 @@ EXPORTS = {
                                                ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
                                                ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
                                                ctypes.c_void_p]),
+    "opt2s_mx4_project_row": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32,
+                                             ctypes.POINTER(opt2s_mx4), ctypes.c_void_p, ctypes.c_int32,
+                                             ctypes.c_void_p]),
     "opt2s_step_mx4": (ctypes.c_int, [ctypes.POINTER(TensorListDescMx4), ctypes.POINTER(Hyper), ctypes.c_int,
                                       ctypes.c_void_p]),
     "opt2s_mx4_errors": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32)]),

@@ -431,4 +431,17 @@ int64_t step_mx4_tiles(const StepMx4Rec& t);
 cudaError_t launch_step_mx4(const StepMx4Rec* recs, int n, int algo, int skip_zeros, StepScalars s,
                             cudaStream_t stream);
 
+// One row times a 4-bit weight, the row quantised by the kernel.
+struct Mx4RowArgs {
+    const void* x;
+    int64_t cols;
+    const uint8_t* codes;
+    const uint8_t* scales;
+    int64_t w_rows, w_sf_rows;
+    void* d;
+    int32_t vec;                      // x starts on 16 bytes
+};
+constexpr int64_t kRowMaxCols = 32768;        // the row's codes in shared memory: 33 KiB
+cudaError_t launch_mx4_row(const Mx4RowArgs& a, int in, int out, cudaStream_t stream);
+
 }  // namespace opt2s

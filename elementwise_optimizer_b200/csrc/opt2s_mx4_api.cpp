@@ -218,6 +218,32 @@ OPT2S_API int opt2s_mx4_matmul_ragged(const opt2s_mx4* a, const opt2s_mx4* b, co
     return product(a, b, offsets, groups, true, d, groups * a->rows, ldd, dtype, accumulate, 0, stream);
 }
 
+static_assert(OPT2S_MX4_PROJECT_COLS == opt2s::kRowMaxCols, "column limit");
+
+OPT2S_API int opt2s_mx4_project_row(const void* x, int64_t cols, int32_t x_dtype, const opt2s_mx4* w, void* d,
+                                    int32_t dtype, cudaStream_t stream)
+{
+    OPT2S_RANGE("opt2s_mx4_project_row");
+    if (!good_dtype(x_dtype) || !good_dtype(dtype)) return OPT2S_ERR_INVALID_ARG;
+    Range r[4];
+    size_t n = 0;
+    int st = matrix_ranges(w, false, r, &n);
+    if (st != OPT2S_OK) return st;
+    if (w->slabs != 1 || w->cols != cols) return OPT2S_ERR_INVALID_ARG;
+    if (cols > OPT2S_MX4_PROJECT_COLS) return OPT2S_ERR_TOO_LARGE;
+    if (w->rows == 0) return OPT2S_OK;
+    const int xs = opt2s::elem_bytes(x_dtype), es = opt2s::elem_bytes(dtype);
+    if (!x || !aligned(x, xs) || !d || !aligned(d, es)) return OPT2S_ERR_INVALID_ARG;
+    r[n++] = span(x, cols * xs, false);
+    r[n++] = span(d, w->rows * es, true);
+    if ((st = opt2s::overlap_status(r, n)) != OPT2S_OK) return st;
+    const opt2s::Mx4RowArgs a{x, cols, w->codes, w->scales, w->rows, up(w->rows, 4), d, aligned(x, 16)};
+    const cudaError_t e = opt2s::launch_mx4_row(a, x_dtype, dtype, stream);
+    if (e != cudaSuccess) return opt2s::record_cuda_error(e);
+    opt2s::count_launches(1);
+    return OPT2S_OK;
+}
+
 namespace {
 
 // Checks one record of the step, appends its ranges and its kernel record.

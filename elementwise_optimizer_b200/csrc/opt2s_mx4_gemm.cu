@@ -322,58 +322,26 @@ template <int DT> __device__ __forceinline__ uint32_t pack_out(float lo, float h
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Accumulator columns c0 .. c0+N-1 of this thread's lane (row of P).
-template <int N, int DT, bool SWAP>
-__device__ __forceinline__ void store_cols(const Mx4GemmArgs& a, const Tile& t, int lane_row, int c0, const float (&x)[N])
+// Swapped operands: the lane is a column of D, the accumulator's columns c0 ..
+// c0+N-1 are rows of it, so a warp stores 32 neighbouring elements of a row.
+template <int N, int DT>
+__device__ __forceinline__ void store_swapped(const Mx4GemmArgs& a, const Tile& t, int lane_row, int c0, const float (&x)[N])
 {
-    const int cols = static_cast<int>(a.d_cols);
-    if (SWAP) {
-        // the lane is a column of D, the accumulator's columns are its rows:
-        // a warp stores 32 neighbouring elements of one row
-        const int col = t.d_col + lane_row;
-        if (col >= cols) return;
+    const int col = t.d_col + lane_row;
+    if (col >= a.d_cols) return;
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            if (c0 + j >= t.d_rows) break;
-            const int64_t i = (t.d_row + c0 + j) * a.ldd + col;
-            store_out<DT>(a.d, i, a.accumulate ? __fadd_rn(load_out<DT>(a.d, i), x[j]) : x[j]);
-        }
-        return;
+    for (int j = 0; j < N; ++j) {
+        if (c0 + j >= t.d_rows) break;
+        const int64_t i = (t.d_row + c0 + j) * a.ldd + col;
+        store_out<DT>(a.d, i, a.accumulate ? __fadd_rn(load_out<DT>(a.d, i), x[j]) : x[j]);
     }
-    if (lane_row >= t.d_rows) return;
-    const int col = t.d_col + c0;
-    const int64_t i = (t.d_row + lane_row) * a.ldd + col;
-    if (N >= 16 && a.vec && !a.accumulate && col + N <= cols) {
-        // whole 32-byte sectors a lane
-        if (DT == kF32) {
-            uint32_t* d = static_cast<uint32_t*>(a.d) + i;
-#pragma unroll
-            for (int k = 0; k < N; k += 8)
-                store32(d + k, __float_as_uint(x[k]), __float_as_uint(x[k + 1]), __float_as_uint(x[k + 2]),
-                        __float_as_uint(x[k + 3]), __float_as_uint(x[k + 4]), __float_as_uint(x[k + 5]),
-                        __float_as_uint(x[k + 6]), __float_as_uint(x[k + 7]));
-        } else {
-            uint16_t* d = static_cast<uint16_t*>(a.d) + i;
-#pragma unroll
-            for (int k = 0; k < N; k += 16)
-                store32(d + k, pack_out<DT>(x[k], x[k + 1]), pack_out<DT>(x[k + 2], x[k + 3]),
-                        pack_out<DT>(x[k + 4], x[k + 5]), pack_out<DT>(x[k + 6], x[k + 7]),
-                        pack_out<DT>(x[k + 8], x[k + 9]), pack_out<DT>(x[k + 10], x[k + 11]),
-                        pack_out<DT>(x[k + 12], x[k + 13]), pack_out<DT>(x[k + 14], x[k + 15]));
-        }
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-        if (col + j < cols) store_out<DT>(a.d, i + j, a.accumulate ? __fadd_rn(load_out<DT>(a.d, i + j), x[j]) : x[j]);
 }
-
-template <int N, bool SWAP>
-__device__ __forceinline__ void store_any(const Mx4GemmArgs& a, const Tile& t, int lane_row, int c0, const float (&x)[N])
+template <int N>
+__device__ __forceinline__ void store_swapped(const Mx4GemmArgs& a, const Tile& t, int lane_row, int c0, const float (&x)[N])
 {
-    if (a.dtype == kF32) store_cols<N, kF32, SWAP>(a, t, lane_row, c0, x);
-    else if (a.dtype == kF16) store_cols<N, kF16, SWAP>(a, t, lane_row, c0, x);
-    else store_cols<N, kBF16, SWAP>(a, t, lane_row, c0, x);
+    if (a.dtype == kF32) store_swapped<N, kF32>(a, t, lane_row, c0, x);
+    else if (a.dtype == kF16) store_swapped<N, kF16>(a, t, lane_row, c0, x);
+    else store_swapped<N, kBF16>(a, t, lane_row, c0, x);
 }
 
 // An epilogue warp's two buffers of 32 rows x 128 bytes (swizzled as the
@@ -430,6 +398,49 @@ struct StoreBuffers {
             else asm volatile("cp.async.bulk.commit_group;" ::: "memory");
         }
         ++used;
+    }
+    // The same columns where rows are missing, D's rows do not start on 32
+    // bytes, or D is added to: through a buffer, each row as 32 neighbouring
+    // elements of a warp (stored by the lanes that hold the rows, 32 rows an
+    // instruction, 999 x 531 x 1,000 into fp32 took 28 us).
+    template <int DT>
+    __device__ __forceinline__ void put_rows_as(const Mx4GemmArgs& a, const Tile& t, int warp, int lane, int c, const float (&x)[32])
+    {
+        float* buf = reinterpret_cast<float*>(base);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) buf[lane * 32 + (k ^ lane)] = x[k];
+        __syncwarp();
+        const int rows = min(32, t.d_rows - (warp & 3) * 32), col = t.d_col + c + lane;
+        if (col < a.d_cols) {
+            const int64_t at = (t.d_row + (warp & 3) * 32) * a.ldd + col;
+            if (a.accumulate) {
+                for (int r0 = 0; r0 < rows; r0 += 8) {       // eight loads in flight
+                    float old[8];
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) old[r] = r0 + r < rows ? load_out<DT>(a.d, at + (r0 + r) * a.ldd) : 0.0f;
+#pragma unroll
+                    for (int r = 0; r < 8; ++r)
+                        if (r0 + r < rows)
+                            store_out<DT>(a.d, at + (r0 + r) * a.ldd, __fadd_rn(old[r], buf[(r0 + r) * 32 + (lane ^ (r0 + r))]));
+                }
+            } else {
+#pragma unroll 8
+                for (int r = 0; r < rows; ++r) store_out<DT>(a.d, at + r * a.ldd, buf[r * 32 + (lane ^ r)]);
+            }
+        }
+        __syncwarp();
+    }
+    __device__ __forceinline__ void put_rows(const Mx4GemmArgs& a, const Tile& t, int warp, int lane, int c, const float (&x)[32])
+    {
+        if (t.d_rows <= (warp & 3) * 32 || t.d_col + c >= a.d_cols) return;
+        // stores of earlier tiles may still read the buffers
+        if (used) {
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            __syncwarp();
+        }
+        if (a.dtype == kF32) put_rows_as<kF32>(a, t, warp, lane, c, x);
+        else if (a.dtype == kF16) put_rows_as<kF16>(a, t, warp, lane, c, x);
+        else put_rows_as<kBF16>(a, t, warp, lane, c, x);
     }
     __device__ __forceinline__ void done(int lane)
     {
@@ -734,7 +745,7 @@ mx4_gemm_kernel(const __grid_constant__ Mx4GemmMaps maps, const Mx4GemmArgs a)
 #pragma unroll
                         for (int i = 0; i < kFirst; ++i) {
                             if (whole) out.put(maps.d, a, o, warp, lane, chunk(i), x[i]);
-                            else store_any<32, SWAP>(a, o, lane_row, chunk(i), x[i]);
+                            else out.put_rows(a, o, warp, lane, chunk(i), x[i]);
                         }
                     }
 #pragma unroll 1
@@ -742,13 +753,9 @@ mx4_gemm_kernel(const __grid_constant__ Mx4GemmMaps maps, const Mx4GemmArgs a)
                         const int c = chunk(i);
                         float x[kChunk];
                         tmem_ld(acc + c, x);
-                        if constexpr (kChunk == 32) {
-                            if (whole) {
-                                out.put(maps.d, a, o, warp, lane, c, x);
-                                continue;
-                            }
-                        }
-                        store_any<kChunk, SWAP>(a, o, lane_row, c, x);
+                        if constexpr (SWAP) store_swapped<kChunk>(a, o, lane_row, c, x);
+                        else if (whole) out.put(maps.d, a, o, warp, lane, c, x);
+                        else out.put_rows(a, o, warp, lane, c, x);
                     }
                     if constexpr (kFirst == 0) {
                         fence_before();
@@ -757,10 +764,12 @@ mx4_gemm_kernel(const __grid_constant__ Mx4GemmMaps maps, const Mx4GemmArgs a)
                     }
                 }
                 ++n;
-            } else if (split == 1 && !a.accumulate) {
-                const float zero[16] = {};
+            } else if (!SWAP && !a.accumulate) {         // an empty group's product
+                if constexpr (!SWAP) {
+                    const float zero[32] = {};
 #pragma unroll 1
-                for (int c = 0; c < BN; c += 16) store_any<16, SWAP>(a, o, lane_row, c, zero);
+                    for (int c = 0; c < BN; c += 32) out.put_rows(a, o, warp, lane, c, zero);
+                }
             }
         }
         out.done(lane);
@@ -817,7 +826,7 @@ mx4_gemm_kernel(const __grid_constant__ Mx4GemmMaps maps, const Mx4GemmArgs a)
                     x[2] = __fadd_rn(x[2], v.z);
                     x[3] = __fadd_rn(x[3], v.w);
                 }
-                store_any<4, SWAP>(a, o, lane_row, 4 * g, x);
+                store_swapped<4>(a, o, lane_row, 4 * g, x);
             }
         }
     }
@@ -945,8 +954,21 @@ cudaError_t launch_mx4_gemm(Mx4GemmArgs a, const Mx4GemmOperands& op, cudaStream
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     a.split = 1;
-    if (a.ragged_k) return a.p_rows > 128 && a.w_rows > 128 ? launch_as<256, false, true>(a, op, sms, stream)
-                                                            : launch_as<128, false, false>(a, op, sms, stream);
+    // 256 x 256 tiles by pairs of CTAs, or 128 x 128 tiles by single ones: the
+    // fewer rounds of tiles, weighted by what a 256-element stage of each takes
+    // (0.42 us for a pair's, 0.30 us for a single's, both bound by the loads),
+    // decide.  256 x 8,192 x 2,048 takes 18 us in pairs and 14 us in singles,
+    // 8,192 x 8,192 x 2,048 68 us in pairs and 85 us in singles.
+    auto pairs_win = [&](int64_t groups, int64_t rows, int64_t cols) {
+        auto rounds = [&](int64_t tile, int64_t at_once) {
+            const int64_t tiles = groups * ((rows + tile - 1) / tile) * ((cols + tile - 1) / tile);
+            return (tiles + at_once - 1) / at_once;
+        };
+        return rounds(256, sms / 2) * 42 <= rounds(128, sms) * 30;
+    };
+    if (a.ragged_k)
+        return pairs_win(a.groups, a.p_rows, a.w_rows) ? launch_as<256, false, true>(a, op, sms, stream)
+                                                       : launch_as<128, false, false>(a, op, sms, stream);
     // Few token rows a group: the weights take the 128-row side of the tile,
     // the tokens its narrow side, and the contraction is cut over a cluster
     // so that the weights' tiles reach every SM.
@@ -955,14 +977,18 @@ cudaError_t launch_mx4_gemm(Mx4GemmArgs a, const Mx4GemmOperands& op, cudaStream
         const int bn = mean <= 16 ? 16 : (mean <= 32 ? 32 : 64);
         const int64_t wt = (a.w_rows + kPRows - 1) / kPRows;
         const int64_t xt = (a.x_rows + bn - 1) / bn + (a.offsets ? std::min<int64_t>(a.groups, a.x_rows) : 0);
-        const int stages = (a.k64 + 3) / 4, most = bn == 16 ? 8 : 4;
-        while (a.split < most && a.split * 2 <= stages && wt * xt * a.split * 2 <= sms) a.split *= 2;
+        // A cluster pays about 1 us to meet at 16 tokens and 3 us at 64, a stage
+        // 0.29 us: 1 x 2,048 x 8,192 takes 12.8 us whole and 8.4 us in four,
+        // 1 x 8,192 x 2,048 6.1 us whole and 7.3 us in two, 64 x 8,192 x 2,048
+        // 6.9 us whole and 11.3 us in two.  So a part keeps 8 stages.
+        const int stages = (a.k64 + 3) / 4;
+        while (a.split < 4 && stages >= a.split * 2 * 8 && wt * xt * a.split * 2 <= sms) a.split *= 2;
         if (bn == 16) return launch_as<16, true, false>(a, op, sms, stream);
         if (bn == 32) return launch_as<32, true, false>(a, op, sms, stream);
         return launch_as<64, true, false>(a, op, sms, stream);
     }
-    if (mean > 128 && a.w_rows > 128) return launch_as<256, false, true>(a, op, sms, stream);
-    return launch_as<128, false, false>(a, op, sms, stream);
+    return pairs_win(a.offsets ? a.groups : 1, mean, a.w_rows) ? launch_as<256, false, true>(a, op, sms, stream)
+                                                               : launch_as<128, false, false>(a, op, sms, stream);
 }
 
 cudaError_t mx4_error_count(unsigned int* out) { return cudaMemcpyFromSymbol(out, g_mx4_errors, sizeof(*out)); }

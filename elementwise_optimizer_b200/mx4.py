@@ -50,7 +50,7 @@ def _extension():
                                "(python -m elementwise_optimizer_b200._build)")
         m.mx4_set_library(*(B.address_of(L, n) for n in (
             "opt2s_mx4_quantize", "opt2s_mx4_dequantize", "opt2s_mx4_matmul", "opt2s_mx4_matmul_grouped",
-            "opt2s_mx4_matmul_ragged")))
+            "opt2s_mx4_matmul_ragged", "opt2s_mx4_project_row")))
         _ext, _ext_lib = m, L
     return _ext
 

@@ -516,6 +516,17 @@ int opt2s_mx4_matmul_ragged(const opt2s_mx4 *a, const opt2s_mx4 *b, const int32_
                             int32_t groups, void *d, int64_t ldd, int32_t dtype,
                             int32_t accumulate, cudaStream_t stream);
 
+/*
+ * opt2s_mx4_project_row  d = Q(x) * w^T for ONE row x in one launch: `cols`
+ * elements at x (type x_dtype) are quantised to nearest by the kernel itself,
+ * as opt2s_mx4_quantize does, and multiplied with w (slabs 1, w->cols ==
+ * cols); sums in fp32 in a fixed order, rounded once to `dtype`.  d: w->rows
+ * elements.  cols <= OPT2S_MX4_PROJECT_COLS (else OPT2S_ERR_TOO_LARGE).
+ */
+#define OPT2S_MX4_PROJECT_COLS 32768
+int opt2s_mx4_project_row(const void *x, int64_t cols, int32_t x_dtype, const opt2s_mx4 *w, void *d,
+                          int32_t dtype, cudaStream_t stream);
+
 /* CTAs of the products that gave up a bounded wait on the current device
  * since the library was loaded (0 unless the hardware or the library is at
  * fault; their outputs are then not written).  Waits for the device. */

@@ -350,6 +350,48 @@ def test_project_matches_linear(mx4):
     assert torch.equal(mx4.project_grouped(x2, mx4.quantize(ws), off), mx4.linear_grouped(x2, ws, off))
 
 
+@pytest.mark.parametrize("n,k", [(1, 32), (17, 100), (300, 2048), (40, 4100), (128, 131), (33, 32768), (5, 32769)])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_project_one_row(mx4, n, k, dtype):
+    """One row of up to 32,768 columns takes a kernel of its own: exact integer
+    sums of each block, fp32 sums over the blocks."""
+    x, w = mixed((1, k), DTYPES[dtype], 141, 0.25), mixed((n, k), torch.float32, 142, 0.25)
+    y, tol = product_bound(round_ref(x), round_ref(w), DTYPES[dtype])
+    close(mx4.project(x, mx4.quantize(w)), y, tol)
+    wide = torch.empty(1, k + 3, dtype=x.dtype, device="cuda")[:, 1:k + 1].copy_(x)      # off 16 bytes
+    assert torch.equal(mx4.project(wide, mx4.quantize(w)), mx4.project(x, mx4.quantize(w)))
+
+
+@pytest.mark.parametrize("counts,extra", [([1, 0, 2, 1], 0), ([0, 7, 0, 0], 1), ([0, 0, 0], 2), ([3, 3, 0, 0, 0], 3)])
+def test_project_grouped_few_rows(mx4, counts, extra):
+    rows, n, k = sum(counts) + extra, 70, 260
+    x, w = mixed((rows, k), torch.bfloat16, 151, 0.25), mixed((len(counts), n, k), torch.float32, 152, 0.25)
+    got = mx4.project_grouped(x, mx4.quantize(w), offsets_of(counts), torch.float32)
+    at = 0
+    for e, c in enumerate(counts):
+        if c:
+            close(got[at:at + c], *product_bound(round_ref(x[at:at + c]), round_ref(w[e]), torch.float32))
+        at += c
+    assert not got[at:].any()
+
+
+@pytest.mark.parametrize("rows", [1, 3])
+def test_scales_at_both_ends_and_nan(mx4, rows):
+    """Scales at both ends of their range, and blocks that are NaN."""
+    w = torch.zeros(3, 64)
+    w[0, :32], w[1, 40], w[2, 3] = 2.0 ** -126, 1.0, 1.0
+    for x0, bad in ((2.0 ** 125, False), (2.0 ** -100, True)):       # 32 * 2^-1 through scales 2^123 and 2^-127
+        x = torch.zeros(rows, 64)
+        x[0, :32] = x0
+        if bad:
+            x[0, 40] = float("nan")
+        got = mx4.project(x.cuda(), mx4.quantize(w.cuda())).cpu()
+        want = round_ref(x) @ round_ref(w).mT
+        assert torch.equal(got.isnan(), want.isnan()) and got[0].isnan().all() == bad
+        if not bad:
+            assert torch.equal(got, want.float()) and got[0, 0].item() == 16.0
+
+
 # ---------------------------------------------------------------------------
 # How they are called
 # ---------------------------------------------------------------------------
