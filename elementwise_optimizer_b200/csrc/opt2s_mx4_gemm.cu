@@ -179,6 +179,15 @@ __device__ __forceinline__ void tmem_ld(uint32_t at, float (&x)[32])
                    "=f"(x[24]), "=f"(x[25]), "=f"(x[26]), "=f"(x[27]), "=f"(x[28]), "=f"(x[29]), "=f"(x[30]), "=f"(x[31])
                  : "r"(at) : "memory");
 }
+// 64 columns at `at` and 32 at `more`, one wait.
+__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t more, float (&x)[3][32])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%96];\n\t"
+                 "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, %80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95}, [%97];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : "=f"(x[0][0]), "=f"(x[0][1]), "=f"(x[0][2]), "=f"(x[0][3]), "=f"(x[0][4]), "=f"(x[0][5]), "=f"(x[0][6]), "=f"(x[0][7]), "=f"(x[0][8]), "=f"(x[0][9]), "=f"(x[0][10]), "=f"(x[0][11]), "=f"(x[0][12]), "=f"(x[0][13]), "=f"(x[0][14]), "=f"(x[0][15]), "=f"(x[0][16]), "=f"(x[0][17]), "=f"(x[0][18]), "=f"(x[0][19]), "=f"(x[0][20]), "=f"(x[0][21]), "=f"(x[0][22]), "=f"(x[0][23]), "=f"(x[0][24]), "=f"(x[0][25]), "=f"(x[0][26]), "=f"(x[0][27]), "=f"(x[0][28]), "=f"(x[0][29]), "=f"(x[0][30]), "=f"(x[0][31]), "=f"(x[1][0]), "=f"(x[1][1]), "=f"(x[1][2]), "=f"(x[1][3]), "=f"(x[1][4]), "=f"(x[1][5]), "=f"(x[1][6]), "=f"(x[1][7]), "=f"(x[1][8]), "=f"(x[1][9]), "=f"(x[1][10]), "=f"(x[1][11]), "=f"(x[1][12]), "=f"(x[1][13]), "=f"(x[1][14]), "=f"(x[1][15]), "=f"(x[1][16]), "=f"(x[1][17]), "=f"(x[1][18]), "=f"(x[1][19]), "=f"(x[1][20]), "=f"(x[1][21]), "=f"(x[1][22]), "=f"(x[1][23]), "=f"(x[1][24]), "=f"(x[1][25]), "=f"(x[1][26]), "=f"(x[1][27]), "=f"(x[1][28]), "=f"(x[1][29]), "=f"(x[1][30]), "=f"(x[1][31]), "=f"(x[2][0]), "=f"(x[2][1]), "=f"(x[2][2]), "=f"(x[2][3]), "=f"(x[2][4]), "=f"(x[2][5]), "=f"(x[2][6]), "=f"(x[2][7]), "=f"(x[2][8]), "=f"(x[2][9]), "=f"(x[2][10]), "=f"(x[2][11]), "=f"(x[2][12]), "=f"(x[2][13]), "=f"(x[2][14]), "=f"(x[2][15]), "=f"(x[2][16]), "=f"(x[2][17]), "=f"(x[2][18]), "=f"(x[2][19]), "=f"(x[2][20]), "=f"(x[2][21]), "=f"(x[2][22]), "=f"(x[2][23]), "=f"(x[2][24]), "=f"(x[2][25]), "=f"(x[2][26]), "=f"(x[2][27]), "=f"(x[2][28]), "=f"(x[2][29]), "=f"(x[2][30]), "=f"(x[2][31])
+                 : "r"(at), "r"(more) : "memory");
+}
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
@@ -473,7 +482,8 @@ mx4_gemm_kernel(const __grid_constant__ Mx4GemmMaps maps, const Mx4GemmArgs a)
     const uint32_t codes_at = smem_u32(smem), sf_at = smem_u32(sf_smem), bar0 = smem_u32(bars);
     auto full = [&](int s) { return bar0 + 8u * s; };
     auto empty = [&](int s) { return bar0 + 8u * (G::kStages + s); };
-    auto sf_full = [&](int s) { return bar0 + 8u * (2 * G::kStages + s); };
+    // a stage's scales are in order, and its codes have landed
+    auto ready = [&](int s) { return bar0 + 8u * (2 * G::kStages + s); };
     // where a stage's scales land: on their own in a pair, whose codes all land on the first CTA's `full`
     auto sf_land = [&](int s) { return bar0 + 8u * (PAIR ? 3 * G::kStages + s : s); };
     auto acc_full = [&](int b) { return bar0 + 8u * (4 * G::kStages + b); };
@@ -494,7 +504,7 @@ mx4_gemm_kernel(const __grid_constant__ Mx4GemmMaps maps, const Mx4GemmArgs a)
         for (int s = 0; s < G::kStages; ++s) {
             bar_init(full(s), 1);
             bar_init(empty(s), 1);
-            bar_init(sf_full(s), PAIR ? 2 : 1);
+            bar_init(ready(s), PAIR ? 2 : 1);
             if (PAIR) bar_init(sf_land(s), 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -604,8 +614,7 @@ mx4_gemm_kernel(const __grid_constant__ Mx4GemmMaps maps, const Mx4GemmArgs a)
                 }
                 const uint32_t d = tmem + b * G::kAccStep;
                 for (int k = 0; k < steps; k += 4) {
-                    if (!(ok = warp_wait(full(s), ph, &abort_flag))) break;
-                    if (!(ok = warp_wait(sf_full(s), ph, &abort_flag))) break;
+                    if (!(ok = warp_wait(ready(s), ph, &abort_flag))) break;
                     if constexpr (G::kSfSlots < G::kStages) {
                         // the slot's last readers: the MMAs of kSfSlots stages before
                         if (ahead < G::kSfSlots) {
@@ -708,7 +717,9 @@ mx4_gemm_kernel(const __grid_constant__ Mx4GemmMaps maps, const Mx4GemmArgs a)
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) arrive_first(sf_full(s));
+                // the pair's codes land on the first CTA's barrier: its arrival says that they are there too
+                if (PAIR && half == 0 && !(ok = warp_wait(full(s), (it / G::kStages) & 1, &abort_flag))) break;
+                if (lane == 0) arrive_first(ready(s));
             }
         }
     } else if (warp >= 8) {
@@ -737,8 +748,7 @@ mx4_gemm_kernel(const __grid_constant__ Mx4GemmMaps maps, const Mx4GemmArgs a)
                     const bool whole = !SWAP && a.tma_store && o.d_rows - (warp & 3) * 32 >= 32;
                     if constexpr (kFirst > 0) {
                         float x[kFirst][32];
-#pragma unroll
-                        for (int i = 0; i < kFirst; ++i) tmem_ld(acc + chunk(i), x[i]);
+                        tmem_ld(acc + chunk(0), acc + chunk(2), x);
                         fence_before();
                         __syncwarp();
                         if (lane == 0) arrive_first(acc_empty(b));
