@@ -4,6 +4,7 @@
 #pragma once
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -301,6 +302,22 @@ struct Range {
     uintptr_t lo, hi;
     bool written;
 };
+
+// Lets kernel `k` take `bytes` of dynamic shared memory on the current device.
+// An attribute of a function stays with the device, so it is set once for each
+// (by whichever thread comes first; setting it twice does no harm).
+template <typename K>
+inline cudaError_t allow_shared(K* k, int bytes, std::atomic<uint64_t>& done)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = uint64_t{1} << (dev & 63);
+    if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 // Checks one record of a collection stepped with `algo` and writes the
 // ranges of its four buffers to out[0..3] (*n = 4), or *n = 0 for an empty

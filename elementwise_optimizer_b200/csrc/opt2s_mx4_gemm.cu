@@ -939,7 +939,8 @@ cudaError_t launch_as(Mx4GemmArgs a, const Mx4GemmOperands& op, int sms, cudaStr
     const int cluster = PAIR ? 2 : a.split;
     const int64_t ctas = a.split > 1 ? tiles * cluster : std::min<int64_t>(tiles, sms / cluster * kResident) * cluster;
     auto* k = mx4_gemm_kernel<BN, SWAP, PAIR>;
-    if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem)) != cudaSuccess) return e;
+    static std::atomic<uint64_t> allowed{0};
+    if ((e = allow_shared(k, G::kSmem, allowed)) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas));
     cfg.blockDim = dim3(kThreads);

@@ -230,8 +230,8 @@ cudaError_t launch_quantize_as(const Mx4QuantArgs& a, dim3 grid, cudaStream_t st
 {
     constexpr int kBytes = kTileRows * kTileCols * (Src<DT>::kBytes + (NOISE ? 1 : 0));
     auto* k = mx4_quantize_kernel<DT, NOISE>;
-    // an attribute of the function on the current device: set at every launch, it costs no synchronisation
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e = allow_shared(k, kBytes, allowed);
     if (e != cudaSuccess) return e;
     k<<<grid, kQuantThreads, kBytes, stream>>>(a);
     return cudaGetLastError();

@@ -72,6 +72,30 @@ struct Matrix {
     }
 };
 
+// A matrix of the extension's own: codes and scales in one allocation.
+struct Packed {
+    Tensor buffer;
+    opt2s_mx4 c{};
+};
+
+int64_t code_bytes(int64_t slabs, int64_t rows, int64_t cols) { return slabs * rows * (up(cols, 128) / 2); }
+
+opt2s_mx4 packed_view(const Tensor& buffer, int64_t slabs, int64_t rows, int64_t cols)
+{
+    uint8_t* at = buffer.data_ptr<uint8_t>();
+    return {at, at + code_bytes(slabs, rows, cols), slabs, rows, cols};      // code rows are multiples of 64 bytes
+}
+
+Packed packed(int64_t slabs, int64_t rows, int64_t cols, const at::Device& device)
+{
+    const int64_t bytes = code_bytes(slabs, rows, cols) + up(cols, 128) / 128 * slabs * up(rows, 4) * 4;
+    Packed p;
+    p.buffer = at::empty({bytes}, at::TensorOptions().dtype(at::kByte).device(device));
+    if (bytes) p.c = packed_view(p.buffer, slabs, rows, cols);
+    else p.c = {nullptr, nullptr, slabs, rows, cols};
+    return p;
+}
+
 Matrix empty_matrix(int64_t slabs, int64_t rows, int64_t cols, const at::Device& device)
 {
     const auto o = at::TensorOptions().dtype(at::kByte).device(device);
@@ -92,9 +116,15 @@ int32_t check_offsets(const Tensor& offsets, const at::Device& device)
 
 cudaStream_t stream_of(const at::Device& d) { return c10::cuda::getCurrentCUDAStream(d.index()).stream(); }
 
-// x (2-D, or 3-D slabs) into q and/or qt, allocated where they are wanted and
-// not given.
-void quantize(const Tensor& x, const OptTensor& noise, const OptTensor& offsets, Matrix* q, Matrix* qt)
+// What a quantisation of x (2-D, or 3-D slabs) gets and gives.
+struct Job {
+    opt2s_mx4_source src;
+    const int32_t* offsets = nullptr;
+    int32_t groups = 0;
+    int64_t t_cols;              // columns of the transposed form
+};
+
+Job job_of(const Tensor& x, const OptTensor& noise, const OptTensor& offsets)
 {
     TORCH_CHECK_VALUE(x.is_cuda(), "a tensor to quantise must be on a CUDA device");
     TORCH_CHECK_VALUE(x.dim() == 2 || x.dim() == 3, "a tensor to quantise has 2 dimensions, or 3 with slabs");
@@ -108,36 +138,56 @@ void quantize(const Tensor& x, const OptTensor& noise, const OptTensor& offsets,
                               noise->device() == x.device(),
                           "noise must be a contiguous uint8 tensor of the source's shape and device");
     }
-    int32_t groups = 0;
+    Job j;
     if (offsets) {
-        groups = check_offsets(*offsets, x.device());
+        j.groups = check_offsets(*offsets, x.device());
+        j.offsets = offsets->data_ptr<int32_t>();
         TORCH_CHECK_VALUE(slabs == 1, "only a single matrix is cut into groups of rows");
     }
-    const opt2s_mx4_source src{x.data_ptr(), noise ? noise->data_ptr<uint8_t>() : nullptr, slabs, rows, cols,
-                               x.stride(-2), three ? x.stride(0) : 0, dtype_code(x.scalar_type()), 0};
-    const int64_t t_cols = groups ? up(rows, 128) + 128 * groups : rows;
+    j.src = {x.data_ptr(), noise ? noise->data_ptr<uint8_t>() : nullptr, slabs, rows, cols,
+             x.stride(-2), three ? x.stride(0) : 0, dtype_code(x.scalar_type()), 0};
+    j.t_cols = j.groups ? up(rows, 128) + 128 * j.groups : rows;
+    return j;
+}
+
+// On the current device, which is x's.
+void run_job(const Job& j, const opt2s_mx4* q, const opt2s_mx4* qt, const at::Device& device)
+{
+    check(lib.quantize(&j.src, q, j.t_cols ? qt : nullptr, j.offsets, j.groups, stream_of(device)), "opt2s_mx4_quantize");
+}
+
+// The forms of x that are wanted, for the extension's own use.
+void quantize(const Tensor& x, const OptTensor& noise, const OptTensor& offsets, Packed* q, Packed* qt)
+{
+    const Job j = job_of(x, noise, offsets);
+    const c10::cuda::CUDAGuard guard(x.device());
+    if (q) *q = packed(j.src.slabs, j.src.rows, j.src.cols, x.device());
+    if (qt && j.t_cols) *qt = packed(j.src.slabs, j.src.cols, j.t_cols, x.device());
+    run_job(j, q ? &q->c : nullptr, qt ? &qt->c : nullptr, x.device());
+}
+
+// The same for a caller: into q and/or qt, allocated where they are not given.
+void quantize(const Tensor& x, const OptTensor& noise, const OptTensor& offsets, Matrix* q, Matrix* qt)
+{
+    const Job j = job_of(x, noise, offsets);
     const c10::cuda::CUDAGuard guard(x.device());
     auto fit = [&](Matrix* m, int64_t r, int64_t c) {
         if (!m) return;
-        if (!m->codes.defined()) *m = empty_matrix(slabs, r, c, x.device());
-        TORCH_CHECK_VALUE(m->slabs == slabs && m->rows == r && m->cols == c && m->codes.device() == x.device(),
+        if (!m->codes.defined()) *m = empty_matrix(j.src.slabs, r, c, x.device());
+        TORCH_CHECK_VALUE(m->slabs == j.src.slabs && m->rows == r && m->cols == c && m->codes.device() == x.device(),
                           "out does not fit the source on its device");
     };
-    fit(q, rows, cols);
-    if (t_cols == 0) qt = nullptr;               // no row, no transposed form
-    fit(qt, cols, t_cols);
+    fit(q, j.src.rows, j.src.cols);
+    if (j.t_cols == 0) qt = nullptr;             // no row, no transposed form
+    fit(qt, j.src.cols, j.t_cols);
     const opt2s_mx4 cq = q ? q->c() : opt2s_mx4{}, ct = qt ? qt->c() : opt2s_mx4{};
-    check(lib.quantize(&src, q ? &cq : nullptr, qt ? &ct : nullptr, offsets ? offsets->data_ptr<int32_t>() : nullptr,
-                       groups, stream_of(x.device())),
-          "opt2s_mx4_quantize");
+    run_job(j, q ? &cq : nullptr, qt ? &ct : nullptr, x.device());
 }
 
 // The three products; d is [rows, cols] or [groups, rows, cols].
-Tensor product(const Matrix& a, const Matrix& b, const OptTensor& offsets, bool ragged, c10::ScalarType dtype,
-               const OptTensor& given, bool accumulate)
+Tensor product(const opt2s_mx4& a, const opt2s_mx4& b, const at::Device& device, const OptTensor& offsets, bool ragged,
+               c10::ScalarType dtype, const OptTensor& given, bool accumulate)
 {
-    const at::Device device = a.codes.device();
-    TORCH_CHECK_VALUE(b.codes.device() == device, "a product's operands must be on one device");
     TORCH_CHECK_VALUE(a.cols == b.cols, "the contractions differ: ", a.cols, " and ", b.cols);
     TORCH_CHECK_VALUE(a.slabs == 1, "the first operand of a product is a single matrix");
     int32_t groups = 0;
@@ -163,15 +213,14 @@ Tensor product(const Matrix& a, const Matrix& b, const OptTensor& offsets, bool 
         TORCH_CHECK_VALUE(!accumulate, "accumulate needs the tensor to add to (out)");
         d = at::empty(shape, at::TensorOptions().dtype(dtype).device(device));
     }
-    const opt2s_mx4 ca = a.c(), cb = b.c();
     const int32_t code = dtype_code(d.scalar_type()), acc = accumulate ? 1 : 0;
     void* out = d.numel() ? d.data_ptr() : nullptr;
     const cudaStream_t s = stream_of(device);
-    if (!offsets) check(lib.matmul(&ca, &cb, out, ldd, code, acc, s), "opt2s_mx4_matmul");
+    if (!offsets) check(lib.matmul(&a, &b, out, ldd, code, acc, s), "opt2s_mx4_matmul");
     else if (ragged)
-        check(lib.matmul_ragged(&ca, &cb, offsets->data_ptr<int32_t>(), groups, out, ldd, code, acc, s), "opt2s_mx4_matmul_ragged");
+        check(lib.matmul_ragged(&a, &b, offsets->data_ptr<int32_t>(), groups, out, ldd, code, acc, s), "opt2s_mx4_matmul_ragged");
     else
-        check(lib.matmul_grouped(&ca, &cb, offsets->data_ptr<int32_t>(), groups, out, ldd, code, acc, given ? 0 : 1, s),
+        check(lib.matmul_grouped(&a, &b, offsets->data_ptr<int32_t>(), groups, out, ldd, code, acc, given ? 0 : 1, s),
               "opt2s_mx4_matmul_grouped");
     return d;
 }
@@ -183,9 +232,9 @@ Tensor rows_of(const Tensor& x)
     return m.size(-1) <= 1 || m.stride(-1) == 1 ? m : m.contiguous();
 }
 
-Tensor times(const Matrix& a, const Matrix& b, const OptTensor& offsets, c10::ScalarType dtype)
+Tensor times(const opt2s_mx4& a, const opt2s_mx4& b, const at::Device& device, const OptTensor& offsets, c10::ScalarType dtype)
 {
-    return product(a, b, offsets, false, dtype, std::nullopt, false);
+    return product(a, b, device, offsets, false, dtype, std::nullopt, false);
 }
 
 Tensor project(const Tensor& x, const Matrix& w, const OptTensor& offsets, std::optional<c10::ScalarType> dtype)
@@ -210,9 +259,9 @@ Tensor project(const Tensor& x, const Matrix& w, const OptTensor& offsets, std::
                               dtype_code(out), stream_of(device)),
               "opt2s_mx4_project_row");
     } else {
-        Matrix q;
+        Packed q;
         quantize(rows, std::nullopt, std::nullopt, &q, nullptr);
-        y = times(q, w, offsets, out);
+        y = times(q.c, w.c(), device, offsets, out);
     }
     if (x.dim() == 2) return y;
     std::vector<int64_t> shape = x.sizes().vec();
@@ -225,26 +274,35 @@ Tensor project(const Tensor& x, const Matrix& w, const OptTensor& offsets, std::
 struct Linear : torch::autograd::Function<Linear> {
     using Ctx = torch::autograd::AutogradContext;
 
-    static Tensor forward(Ctx* ctx, const Tensor& x, const Tensor& weight, const OptTensor& offsets, Matrix wq, Matrix wt,
-                          const OptTensor& noise, bool need_x, bool need_w)
+    // Saved: the weight's and x's transposed forms, each as codes and scales (a
+    // kept copy) or one buffer, and the shapes in one list.
+    static Tensor forward(Ctx* ctx, const Tensor& x, const Tensor& weight, const OptTensor& offsets, const Matrix& wq,
+                          const Matrix& wt, const OptTensor& noise, bool need_x, bool need_w)
     {
-        if (!wq.codes.defined()) quantize(weight, std::nullopt, std::nullopt, &wq, need_x ? &wt : nullptr);
+        const at::Device device = x.device();
+        Packed own_q, own_t, xq, xt;
+        opt2s_mx4 w;
+        if (wq.codes.defined()) {
+            w = wq.c();
+        } else {
+            quantize(weight, std::nullopt, std::nullopt, &own_q, need_x ? &own_t : nullptr);
+            w = own_q.c;
+        }
         const Tensor rows = rows_of(x);
-        Matrix xq, xt;
         quantize(rows, std::nullopt, need_w ? offsets : std::nullopt, &xq, need_w ? &xt : nullptr);
         if (need_x || need_w) {
-            ctx->save_for_backward({need_x ? wt.codes : Tensor(), need_x ? wt.scales : Tensor(), xt.codes, xt.scales,
-                                    offsets ? *offsets : Tensor(), noise ? *noise : Tensor()});
-            ctx->saved_data["x_shape"] = x.sizes().vec();
-            ctx->saved_data["w_shape"] = weight.sizes().vec();
-            ctx->saved_data["w_dtype"] = static_cast<int64_t>(weight.scalar_type());
-            ctx->saved_data["need"] = static_cast<int64_t>(need_x) | static_cast<int64_t>(need_w) << 1;
-            ctx->saved_data["t_cols"] = xt.cols;
+            const bool kept = wq.codes.defined();
+            ctx->save_for_backward({need_x ? (kept ? wt.codes : own_t.buffer) : Tensor(), need_x && kept ? wt.scales : Tensor(),
+                                    xt.buffer, offsets ? *offsets : Tensor(), noise ? *noise : Tensor()});
+            std::vector<int64_t> facts{need_x, need_w, static_cast<int64_t>(weight.scalar_type()), xt.c.cols, weight.dim()};
+            facts.insert(facts.end(), weight.sizes().begin(), weight.sizes().end());
+            facts.insert(facts.end(), x.sizes().begin(), x.sizes().end());
+            ctx->saved_data["facts"] = std::move(facts);
         }
-        Tensor y = times(xq, wq, offsets, x.scalar_type());
+        Tensor y = times(xq.c, w, device, offsets, x.scalar_type());
         if (x.dim() == 2) return y;
         std::vector<int64_t> shape = x.sizes().vec();
-        shape.back() = wq.rows;
+        shape.back() = w.rows;
         return y.view(shape);
     }
 
@@ -255,26 +313,31 @@ struct Linear : torch::autograd::Function<Linear> {
                                     "a 4-bit layer's gradient has no gradient of its own");
         at::NoGradGuard no_grad;
         const auto saved = ctx->get_saved_variables();
-        const auto x_shape = ctx->saved_data["x_shape"].toIntVector(), w_shape = ctx->saved_data["w_shape"].toIntVector();
-        const auto w_dtype = static_cast<c10::ScalarType>(ctx->saved_data["w_dtype"].toInt());
-        const int64_t need = ctx->saved_data["need"].toInt();
-        const bool need_x = need & 1, need_w = need & 2;
-        const OptTensor offsets = saved[4].defined() ? OptTensor(saved[4]) : std::nullopt;
-        const OptTensor noise = saved[5].defined() ? OptTensor(saved[5]) : std::nullopt;
+        const auto facts = ctx->saved_data["facts"].toIntVector();
+        const bool need_x = facts[0], need_w = facts[1];
+        const auto w_dtype = static_cast<c10::ScalarType>(facts[2]);
+        const auto w_at = facts.begin() + 5, x_at = w_at + facts[4];
+        const at::IntArrayRef w_shape(&*w_at, static_cast<size_t>(facts[4]));
+        const at::IntArrayRef x_shape(&*x_at, static_cast<size_t>(facts.end() - x_at));
+        const OptTensor offsets = saved[3].defined() ? OptTensor(saved[3]) : std::nullopt;
+        const OptTensor noise = saved[4].defined() ? OptTensor(saved[4]) : std::nullopt;
         const int64_t n = w_shape[w_shape.size() - 2], k = w_shape.back(), slabs = w_shape.size() == 3 ? w_shape[0] : 1;
+        const at::Device device = dy.device();
         Tensor dx, dw;
         const Tensor rows = rows_of(dy);
         if (rows.size(0) == 0) {
             if (need_x) dx = at::zeros(x_shape, dy.options());
             if (need_w) dw = at::zeros(w_shape, dy.options().dtype(w_dtype));
         } else {
-            Matrix dq, dt;
+            Packed dq, dt;
             quantize(rows, noise, need_w ? offsets : std::nullopt, need_x ? &dq : nullptr, need_w ? &dt : nullptr);
-            if (need_x) dx = times(dq, Matrix{saved[0], saved[1], slabs, k, n}, offsets, dy.scalar_type()).view(x_shape);
-            if (need_w) {
-                const Matrix xt{saved[2], saved[3], 1, k, ctx->saved_data["t_cols"].toInt()};
-                dw = product(dt, xt, offsets, offsets.has_value(), w_dtype, std::nullopt, false);
+            if (need_x) {
+                const opt2s_mx4 wt = saved[1].defined() ? Matrix{saved[0], saved[1], slabs, k, n}.c() : packed_view(saved[0], slabs, k, n);
+                dx = times(dq.c, wt, device, offsets, dy.scalar_type());
+                if (x_shape.size() != 2) dx = dx.view(x_shape);
             }
+            if (need_w)
+                dw = product(dt.c, packed_view(saved[2], 1, k, facts[3]), device, offsets, offsets.has_value(), w_dtype, std::nullopt, false);
         }
         return {dx, dw, Tensor(), Tensor(), Tensor(), Tensor(), Tensor(), Tensor()};
     }
@@ -372,7 +435,9 @@ void bind_mx4(py::module& m)
                             std::optional<at::ScalarType> dtype, const OptTensor& out, bool accumulate) {
         TORCH_CHECK_VALUE(!out || !dtype || out->scalar_type() == *dtype, "out has another dtype than the one asked for");
         at::NoGradGuard no_grad;
-        return product(matrix(a), matrix(b), offsets, ragged, dtype.value_or(at::kBFloat16), out, accumulate);
+        const Matrix ma = matrix(a), mb = matrix(b);
+        TORCH_CHECK_VALUE(ma.codes.device() == mb.codes.device(), "a product's operands must be on one device");
+        return product(ma.c(), mb.c(), ma.codes.device(), offsets, ragged, dtype.value_or(at::kBFloat16), out, accumulate);
     });
     m.def("mx4_project", [](const Tensor& x, const Fields& w, const OptTensor& offsets,
                             std::optional<at::ScalarType> dtype) { return project(x, matrix(w), offsets, dtype);
