@@ -391,13 +391,14 @@ class TensorListMX4:
                                             s or None, ct or None, st or None)
         self.desc = TensorListDescMx4(ctypes.cast(self._arr, ctypes.POINTER(opt2s_tensor_mx4)), n)
         self.count = n
+        self.written = []
 
     @classmethod
     def from_tensors(cls, params, grads, state1, state2, copies) -> "TensorListMX4":
         """From torch tensors; copies[i] is None, or the pair of MX4Tensors
         (blocks along the rows, transposed) that the step keeps up to date for
         a param of 2 dimensions (3 with slabs); either may be None."""
-        recs = []
+        recs, written = [], []
         for p, g, s1, s2, pair in zip(params, grads, state1, state2, copies):
             for t in (p, g, s1, s2):
                 if not t.is_contiguous():
@@ -415,8 +416,11 @@ class TensorListMX4:
                     if (q.slabs, q.rows, q.cols) != want or q.device != p.device:
                         raise ValueError(f"copy {q.shape} is not one of a param {tuple(p.shape)} on its device")
                     ptrs[2 * i:2 * i + 2] = _ptr(q.codes), _ptr(q.scales)
+                    written.append(q.codes)
             recs.append((_ptr(p), _ptr(g), _ptr(s1), _ptr(s2), p.numel(), _torch_dtype_code(p), dims, *ptrs))
-        return cls(recs)
+        tl = cls(recs)
+        tl.written = written             # the copies' code tensors, which a step writes
+        return tl
 
 
 def make_hyper(algo: str = "adam", lr: float = 1e-3, beta1: float = 0.9,

@@ -160,8 +160,8 @@ OPT2S_API int opt2s_mx4_quantize(const opt2s_mx4_source* src, const opt2s_mx4* q
     if (qt) { a.codes_t = qt->codes; a.scales_t = qt->scales; }
     a.offsets = offsets;
     a.groups = groups;
-    a.vec = aligned(src->x, 16) && src->row_stride * es % 16 == 0 && src->slab_stride * es % 16 == 0;
-    a.noise_vec = aligned(src->noise, 16) && src->cols % 16 == 0;
+    a.vec = src->rows > 0 && aligned(src->x, 16) && src->row_stride * es % 16 == 0 && src->slab_stride * es % 16 == 0;
+    a.noise_vec = src->rows > 0 && aligned(src->noise, 16) && src->cols % 16 == 0;
     const cudaError_t e = opt2s::launch_mx4_quantize(a, src->dtype, row_tiles, stream);
     if (e != cudaSuccess) return opt2s::record_cuda_error(e);
     opt2s::count_launches(1);

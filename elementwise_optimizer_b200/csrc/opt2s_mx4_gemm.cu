@@ -27,7 +27,7 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kPRows = 128;
-constexpr uint32_t kWaitLimit = 1u << 22;   // try_wait attempts, each suspending for up to microseconds
+constexpr uint32_t kWaitLimit = 1u << 25;   // attempts; a wait that nothing ends gives up after about a second
 
 __device__ unsigned int g_mx4_errors;
 
@@ -858,16 +858,19 @@ using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, 
 
 cudaError_t encoder(EncodeTiled* out)
 {
-    static EncodeTiled found = nullptr;         // the driver's entry point: the same for every device and thread
-    if (!found) {
-        void* fn = nullptr;
+    // the driver's entry point: the same for every device and thread
+    static std::atomic<EncodeTiled> found{nullptr};
+    EncodeTiled fn = found.load(std::memory_order_relaxed);
+    if (!fn) {
+        void* p = nullptr;
         cudaDriverEntryPointQueryResult q;
-        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q);
         if (e != cudaSuccess) return e;
-        if (!fn || q != cudaDriverEntryPointSuccess) return cudaErrorNotSupported;
-        found = reinterpret_cast<EncodeTiled>(fn);
+        if (!p || q != cudaDriverEntryPointSuccess) return cudaErrorNotSupported;
+        fn = reinterpret_cast<EncodeTiled>(p);
+        found.store(fn, std::memory_order_relaxed);
     }
-    *out = found;
+    *out = fn;
     return cudaSuccess;
 }
 

@@ -48,6 +48,20 @@ void check(int status, const char* where)
     if (status != OPT2S_OK) throw CallFailed(where, status);
 }
 
+// Message texts without streams: formatting numbers through an ostream of the
+// compiler's libstdc++ crashes beside the older one that python has loaded.
+std::string text(const char* s) { return s; }
+std::string text(int64_t n) { return std::to_string(n); }
+std::string text(const at::Device& d) { return d.str(); }
+std::string text(at::IntArrayRef sizes)
+{
+    std::string out = "[";
+    for (size_t i = 0; i < sizes.size(); ++i) out += (i ? ", " : "") + std::to_string(sizes[i]);
+    return out + "]";
+}
+template <typename... A>
+std::string message(const A&... parts) { return (text(parts) + ...); }
+
 int64_t up(int64_t x, int64_t k) { return (x + k - 1) / k * k; }
 
 int32_t dtype_code(c10::ScalarType t)
@@ -58,7 +72,7 @@ int32_t dtype_code(c10::ScalarType t)
     case c10::ScalarType::BFloat16: return OPT2S_BF16;
     default: break;
     }
-    TORCH_CHECK_TYPE(false, "unsupported dtype ", t, " (float32, float16 or bfloat16 are supported)");
+    TORCH_CHECK_TYPE(false, message("unsupported dtype ", c10::toString(t), " (float32, float16 or bfloat16 are supported)"));
 }
 
 // A 4-bit matrix: MX4Tensor's fields.
@@ -109,8 +123,8 @@ int32_t check_offsets(const Tensor& offsets, const at::Device& device)
                           offsets.device() == device,
                       "offsets must be a contiguous 1-D int32 tensor on the operands' device");
     const int64_t groups = offsets.numel() - 1;
-    TORCH_CHECK_VALUE(groups >= 1 && groups <= OPT2S_MX4_MAX_GROUPS, "offsets must hold 2 to ",
-                      OPT2S_MX4_MAX_GROUPS + 1, " values");
+    TORCH_CHECK_VALUE(groups >= 1 && groups <= OPT2S_MX4_MAX_GROUPS, message("offsets must hold 2 to ",
+                      int64_t{OPT2S_MX4_MAX_GROUPS + 1}, " values"));
     return static_cast<int32_t>(groups);
 }
 
@@ -188,12 +202,12 @@ void quantize(const Tensor& x, const OptTensor& noise, const OptTensor& offsets,
 Tensor product(const opt2s_mx4& a, const opt2s_mx4& b, const at::Device& device, const OptTensor& offsets, bool ragged,
                c10::ScalarType dtype, const OptTensor& given, bool accumulate)
 {
-    TORCH_CHECK_VALUE(a.cols == b.cols, "the contractions differ: ", a.cols, " and ", b.cols);
+    TORCH_CHECK_VALUE(a.cols == b.cols, message("the contractions differ: ", a.cols, " and ", b.cols));
     TORCH_CHECK_VALUE(a.slabs == 1, "the first operand of a product is a single matrix");
     int32_t groups = 0;
     if (offsets) groups = check_offsets(*offsets, device);
     const int64_t b_slabs = offsets && !ragged ? groups : 1;
-    TORCH_CHECK_VALUE(b.slabs == b_slabs, "the second operand has ", b.slabs, " slabs where this product takes ", b_slabs);
+    TORCH_CHECK_VALUE(b.slabs == b_slabs, message("the second operand has ", b.slabs, " slabs where this product takes ", b_slabs));
     if (ragged)
         TORCH_CHECK_VALUE(a.cols >= 128 * groups && a.cols % 128 == 0, "the operands were not quantised with these offsets");
     const std::vector<int64_t> shape =
@@ -208,7 +222,7 @@ Tensor product(const opt2s_mx4& a, const opt2s_mx4& b, const at::Device& device,
         if (fits && a.rows > 1) ldd = d.stride(-2);
         else if (fits && ragged && groups > 1) ldd = d.stride(0);
         fits = fits && ldd >= b.rows && (n < 3 || groups <= 1 || a.rows == 0 || d.stride(0) == a.rows * ldd);
-        TORCH_CHECK_VALUE(fits, "out must be ", at::IntArrayRef(shape), " with contiguous, evenly spaced rows on ", device);
+        TORCH_CHECK_VALUE(fits, message("out must be ", at::IntArrayRef(shape), " with contiguous, evenly spaced rows on ", device));
     } else {
         TORCH_CHECK_VALUE(!accumulate, "accumulate needs the tensor to add to (out)");
         d = at::empty(shape, at::TensorOptions().dtype(dtype).device(device));
@@ -240,13 +254,13 @@ Tensor times(const opt2s_mx4& a, const opt2s_mx4& b, const at::Device& device, c
 Tensor project(const Tensor& x, const Matrix& w, const OptTensor& offsets, std::optional<c10::ScalarType> dtype)
 {
     TORCH_CHECK_VALUE(x.is_cuda(), "a tensor to quantise must be on a CUDA device");
-    TORCH_CHECK_VALUE(x.dim() >= 1 && x.size(-1) == w.cols && (!offsets || x.dim() == 2), "x ", x.sizes(),
-                      " does not fit a weight of ", w.rows, " x ", w.cols);
+    TORCH_CHECK_VALUE(x.dim() >= 1 && x.size(-1) == w.cols && (!offsets || x.dim() == 2), message("x ", x.sizes(),
+                      " does not fit a weight of ", w.rows, " x ", w.cols));
     at::NoGradGuard no_grad;
     const at::Device device = x.device();
     TORCH_CHECK_VALUE(w.codes.device() == device, "a product's operands must be on one device");
     const int32_t groups = offsets ? check_offsets(*offsets, device) : 0, slabs = offsets ? groups : 1;
-    TORCH_CHECK_VALUE(w.slabs == slabs, "the weight has ", w.slabs, " slabs where this product takes ", slabs);
+    TORCH_CHECK_VALUE(w.slabs == slabs, message("the weight has ", w.slabs, " slabs where this product takes ", slabs));
     const c10::ScalarType out = dtype.value_or(x.scalar_type());
     const Tensor rows = rows_of(x);
     Tensor y;
@@ -348,7 +362,7 @@ Tensor linear(const Tensor& x, const Tensor& weight, const OptTensor& offsets, c
 {
     TORCH_CHECK_VALUE(weight.dim() == (offsets ? 3 : 2) && x.dim() >= 1 && (!offsets || x.dim() == 2) &&
                           x.size(-1) == weight.size(-1),
-                      "x ", x.sizes(), " does not fit the weight ", weight.sizes());
+                      message("x ", x.sizes(), " does not fit the weight ", weight.sizes()));
     TORCH_CHECK_VALUE(x.is_cuda() && x.device() == weight.device(), "x and weight must be on one CUDA device");
     const int64_t n = weight.size(-2);
     TORCH_CHECK_VALUE(n >= 1, "a layer has at least one output");
@@ -359,7 +373,7 @@ Tensor linear(const Tensor& x, const Tensor& weight, const OptTensor& offsets, c
         const int64_t slabs = weight.dim() == 3 ? weight.size(0) : 1, k = weight.size(-1);
         TORCH_CHECK_VALUE(wq.slabs == slabs && wq.rows == n && wq.cols == k && wt.slabs == slabs && wt.rows == k && wt.cols == n &&
                               wq.codes.device() == x.device() && wt.codes.device() == x.device(),
-                          "copies are not those of a weight ", weight.sizes());
+                          message("copies are not those of a weight ", weight.sizes()));
     }
     OptTensor bytes;
     if (noise) {
@@ -367,7 +381,7 @@ Tensor linear(const Tensor& x, const Tensor& weight, const OptTensor& offsets, c
         want.back() = n;
         TORCH_CHECK_VALUE(noise->scalar_type() == at::kByte && noise->sizes() == at::IntArrayRef(want) &&
                               noise->device() == x.device(),
-                          "noise must be a uint8 tensor of the output's shape ", at::IntArrayRef(want), " on ", x.device());
+                          message("noise must be a uint8 tensor of the output's shape ", at::IntArrayRef(want), " on ", x.device()));
         bytes = noise->reshape({-1, n}).contiguous();
     }
     dtype_code(x.scalar_type());

@@ -20,8 +20,10 @@ step writes them, see ``opt2s_step_mx4``), or one from ``quantize_pair``.
 
 All work happens in the kernels of libopt2s.so, on the tensors' device and
 torch's current stream of it; nothing is kept between calls, and every call
-may be captured in a CUDA graph.  Errors raise ``Opt2sError`` (the library's
-status) or ValueError/TypeError for arguments that do not fit together.
+may be captured in a CUDA graph (a backward pass as torch allows it: while it
+is captured, no graph of the same leaves made outside may be alive).  Errors
+raise ``Opt2sError`` (the library's status) or ValueError/TypeError for
+arguments that do not fit together.
 """
 from __future__ import annotations
 
@@ -149,6 +151,7 @@ def quantize_pair(x: torch.Tensor, noise: torch.Tensor | None = None, offsets: t
     oq, ot = (None, None) if out is None else (_fields(out[0]), _fields(out[1]))
     q, t = _extension().mx4_quantize(x, noise, offsets, True, True, oq, ot)
     if out is not None:
+        torch.autograd.graph.increment_version([m.codes for m in out])
         return tuple(out)
     return MX4Tensor._made(q, x.dim() == 3), MX4Tensor._made(t, x.dim() == 3)
 

@@ -161,6 +161,60 @@ def test_quantize_grouped(mx4, counts, extra):
 # Products
 # ---------------------------------------------------------------------------
 
+def gpu_close(got, a, b):
+    """product_bound with the 64-bit reference on the GPU."""
+    y, mag = a @ b.mT, a.abs() @ b.abs().mT
+    tol = a.shape[-1] * 2.0 ** -23 * mag
+    tol = tol + torch.finfo(got.dtype).eps / 2 * (y.abs() + tol)
+    assert ((got.double() - y).abs() <= tol).all()
+
+
+# every variant of the product over several rounds of its pipeline and, where
+# the launch is persistent, of tiles: (rows, weight rows, columns)
+LONG = [(2100, 4100, 2048), (1500, 3000, 3300), (16, 40000, 1536), (16, 300, 8192), (30, 20000, 2048), (30, 200, 16384),
+        (60, 20100, 2048), (128, 40000, 1600), (100, 260, 9000), (3, 2048, 8192)]
+
+
+@pytest.mark.parametrize("m,n,k", LONG)
+def test_matmul_long(mx4, m, n, k):
+    """With cold and warm caches, bit for bit the same every time."""
+    g = torch.Generator(device="cuda").manual_seed(m + n + k)
+    a, b = (mx4.quantize(torch.randn(r, k, generator=g, device="cuda")) for r in (m, n))
+    flush = torch.empty(64 << 20, device="cuda")
+    first = None
+    for i in range(6):
+        if i % 2 == 0:
+            flush.normal_(generator=g)
+        d = mx4.matmul(a, b, torch.float32 if i < 4 else torch.bfloat16)
+        if first is None:
+            first = d
+            gpu_close(d, a.dequantize().double(), b.dequantize().double())
+        assert torch.equal(d, first.to(d.dtype))
+
+
+@pytest.mark.parametrize("groups,tokens,n,k", [(5, 3000, 700, 1500), (40, 1500, 520, 1300), (130, 100, 300, 2048)])
+def test_grouped_long(mx4, groups, tokens, n, k):
+    r = np.random.RandomState(groups)
+    share = np.exp(1.5 * r.standard_normal(groups))
+    counts = r.multinomial(tokens, share / share.sum()).tolist()
+    g = torch.Generator(device="cuda").manual_seed(groups)
+    x, dy = torch.randn(tokens, k, generator=g, device="cuda"), torch.randn(tokens, n, generator=g, device="cuda")
+    w = mx4.quantize(torch.randn(groups, n, k, generator=g, device="cuda"))
+    off = offsets_of(counts)
+    xq, xt = mx4.quantize_pair(x, offsets=off)
+    dt = mx4.quantize_pair(dy, offsets=off)[1]
+    xv, wv, xtv, dtv = (t.dequantize().double() for t in (xq, w, xt, dt))
+    flush = torch.empty(64 << 20, device="cuda")
+    for i in range(3):
+        flush.normal_(generator=g)
+        y, dw = mx4.matmul_grouped(xq, w, off, torch.float32), mx4.matmul_ragged(dt, xt, off, torch.float32)
+        at = col = 0
+        for e, c in enumerate(counts):
+            gpu_close(y[at:at + c], xv[at:at + c], wv[e])
+            gpu_close(dw[e], dtv[:, col:col + c], xtv[:, col:col + c])
+            at, col = at + c, col + up(c, 128)
+
+
 def operand(mx4, rows, cols, seed, slabs=None, dtype=torch.float32):
     x = mixed((rows, cols) if slabs is None else (slabs, rows, cols), dtype, seed, 0.25)
     return x, mx4.quantize(x)
@@ -396,6 +450,102 @@ def test_scales_at_both_ends_and_nan(mx4, rows):
 # How they are called
 # ---------------------------------------------------------------------------
 
+def test_refusals(mx4):
+    """Arguments that do not fit together, on the GPU's tensors."""
+    from elementwise_optimizer_b200 import Opt2sError
+    x, w = mixed((6, 96), torch.float32, 161), mixed((10, 96), torch.float32, 162)
+    ws = mixed((2, 10, 96), torch.float32, 163)
+    xq, wq, wsq = mx4.quantize(x), mx4.quantize(w), mx4.quantize(ws)
+    off = offsets_of([2, 4])
+    wide = torch.empty(6, 20, device="cuda")
+    bad = [lambda: mx4.quantize(x[0]), lambda: mx4.quantize(x[None, None]), lambda: mx4.quantize(x.t()),
+           lambda: mx4.quantize(x[:, :0]), lambda: mx4.quantize(ws[:0]),
+           lambda: mx4.quantize(x, noise=torch.zeros(6, 95, dtype=torch.uint8, device="cuda")),
+           lambda: mx4.quantize(x, noise=torch.zeros(6, 96, device="cuda")),
+           lambda: mx4.quantize_pair(x, offsets=off.long()), lambda: mx4.quantize_pair(x, offsets=off[:1]),
+           lambda: mx4.quantize_pair(x, offsets=off.cpu()), lambda: mx4.quantize_pair(ws, offsets=off),
+           lambda: mx4.quantize_pair(x, out=mx4.empty_pair(w)),
+           lambda: mx4.quantize_pair(x, offsets=torch.zeros(1026, dtype=torch.int32, device="cuda")),
+           lambda: mx4.matmul(xq, mx4.quantize(w[:, :95])), lambda: mx4.matmul(xq, wsq), lambda: mx4.matmul(wsq, xq),
+           lambda: mx4.matmul(xq, wq, accumulate=True), lambda: mx4.matmul(xq, wq, out=wide),
+           lambda: mx4.matmul(xq, wq, dtype=torch.float32, out=wide[:, :10].bfloat16()),
+           lambda: mx4.matmul(xq, wq, out=wide[:, ::2]), lambda: mx4.matmul_grouped(xq, wsq, offsets_of([1, 2, 3])),
+           lambda: mx4.matmul_grouped(xq, wq, off), lambda: mx4.matmul_ragged(xq, wq, off),
+           lambda: mx4.project(x[:, :95], wq), lambda: mx4.project(x, wsq), lambda: mx4.project_grouped(x, wq, off),
+           lambda: mx4.linear(x, ws), lambda: mx4.linear(x, w.cpu()), lambda: mx4.linear(x, w, copies=mx4.quantize_pair(x)),
+           lambda: mx4.linear(x, w, noise=torch.zeros(6, 9, dtype=torch.uint8, device="cuda")),
+           lambda: mx4.linear_grouped(x, ws, offsets_of([6])), lambda: mx4.linear_grouped(x[None], ws, off),
+           lambda: mx4.linear(x, w[:0])]
+    for i, call in enumerate(bad):
+        with pytest.raises(ValueError):
+            call()
+            pytest.fail(f"call {i} was not refused")
+    for call in (lambda: mx4.quantize(x.double()), lambda: mx4.linear(x.int(), w), lambda: mx4.matmul(x, wq),
+                 lambda: mx4.matmul(xq, wq, dtype=torch.float64), lambda: xq.dequantize(torch.int8)):
+        with pytest.raises(TypeError):
+            call()
+    with pytest.raises(Opt2sError, match="ALIAS"):            # the output in an operand's memory
+        mx4.matmul(xq, wq, out=xq.codes.view(torch.bfloat16).flatten()[:60].view(6, 10))
+    # a copy written between forward and backward, and a gradient of the gradient
+    xg = x.clone().requires_grad_()
+    pair = mx4.quantize_pair(w)
+    y = mx4.linear(xg, w, copies=pair)
+    mx4.quantize_pair(w * 2, out=pair)
+    with pytest.raises(RuntimeError, match="inplace"):
+        y.sum().backward()
+    y = mx4.linear(xg, w)
+    with pytest.raises(NotImplementedError):
+        torch.autograd.grad(y, xg, torch.ones_like(y).requires_grad_(), create_graph=True)
+
+
+@pytest.mark.parametrize("need", [(True, True), (True, False), (False, True)])
+def test_empty_batch_of_experts(mx4, need):
+    x = torch.empty(0, 96, device="cuda", requires_grad=need[0])
+    w = mixed((3, 40, 96), torch.float32, 171).requires_grad_(need[1])
+    y = mx4.linear_grouped(x, w, offsets_of([0, 0, 0]))
+    assert y.shape == (0, 40)
+    y.sum().backward()
+    assert (x.grad is not None and x.grad.shape == x.shape) == need[0]
+    assert not need[1] or (w.grad.shape == w.shape and not w.grad.any())
+
+
+def test_one_dimensional_and_deep_inputs(mx4):
+    x, w = mixed((96,), torch.float32, 181).requires_grad_(), mixed((40, 96), torch.float32, 182)
+    y = mx4.linear(x, w)
+    assert y.shape == (40,) and mx4.project(x, mx4.quantize(w)).shape == (40,)
+    gx, = torch.autograd.grad(y, x, torch.ones(40, device="cuda"))
+    gr, = torch.autograd.grad(mx4.linear(x[None, None], w), x, torch.ones(1, 1, 40, device="cuda"))
+    assert gx.shape == (96,) and torch.equal(gx, gr)
+
+
+def test_past_32_bits(mx4):
+    """A source of 2^32 and some elements, and an output of as many."""
+    rows, cols = 66000, 65536
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x.normal_(generator=g)
+    q, qt = mx4.quantize_pair(x)
+    tail = x[-3:].cpu()
+    v = round_ref(tail)
+    cp = cols // 2
+    codes, scales = encode_ref(tail.double().numpy())
+    raw = q.codes[0, -3:].cpu().numpy()
+    np.testing.assert_array_equal(np.stack((raw & 15, raw >> 4), -1).reshape(3, cols), codes)
+    assert q.codes.shape[-1] == cp
+    raw = qt.codes[0, -2:].cpu().numpy()
+    codes, _ = encode_ref(x[:, -2:].t().cpu().double().numpy())
+    np.testing.assert_array_equal(np.stack((raw & 15, raw >> 4), -1).reshape(2, -1)[:, :rows], codes[:, :rows])
+    got = q.dequantize(torch.bfloat16)
+    assert torch.equal(got[-3:].cpu().double(), v)
+    del got, qt, x
+    a = mx4.quantize(mixed((rows, 64), torch.float32, 191))
+    b = mx4.quantize(mixed((cols, 64), torch.float32, 192))
+    d = mx4.matmul(a, b)
+    want = a.dequantize()[-5:].double().cpu() @ b.dequantize()[-300:].double().cpu().mT
+    close(d[-5:, -300:], want, want.abs() * 2.0 ** -8 + 64 * 2.0 ** -23 * (a.dequantize()[-5:].double().abs().cpu()
+                                                                         @ b.dequantize()[-300:].double().abs().cpu().mT))
+
+
 def test_offsets_out_of_range_stay_in_bounds(mx4):
     """Clamped to the rows and to be non-decreasing: no access out of range,
     and the groups that remain are right."""
@@ -434,6 +584,25 @@ def test_two_streams_at_once(mx4):
     torch.cuda.synchronize()
     for g, y in zip(got, want):
         assert all(torch.equal(v, y) for v in g)
+
+
+def test_every_kernel_at_once(mx4):
+    """Products of all variants, quantisations and a one-row product on five
+    streams together, as often as they fit: the same bits as alone."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    xs = [torch.randn(m, 2048, generator=g, device="cuda").bfloat16() for m in (1, 12, 30, 60, 120, 2100)]
+    w = mx4.quantize(torch.randn(4100, 2048, generator=g, device="cuda"))
+    want = [(mx4.project(x, w), mx4.quantize_pair(x)[1].codes) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(5)]
+    got = []
+    for i in range(40):
+        with torch.cuda.stream(streams[i % 5]):
+            k = i * 7 % len(xs)
+            got.append((k, mx4.project(xs[k], w), mx4.quantize_pair(xs[k])[1].codes))
+    torch.cuda.synchronize()
+    for k, y, codes in got:
+        assert torch.equal(y, want[k][0]) and torch.equal(codes, want[k][1])
 
 
 def test_captured_forward_and_backward(mx4):
