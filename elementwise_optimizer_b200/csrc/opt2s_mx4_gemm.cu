@@ -18,6 +18,8 @@
 // Every wait is bounded: a wait that runs out raises the CTA's abort flag and
 // the library's error flag (opt2s_mx4_errors), and the CTA drains its copies,
 // frees its TMEM and returns.
+#include <type_traits>
+
 #include <cuda.h>
 
 #include "opt2s_mx4.cuh"
@@ -211,7 +213,9 @@ constexpr int round_up(int x, int k) { return (x + k - 1) / k * k; }
 
 template <int BN, bool SWAP, bool PAIR>
 struct Geo {
-    static constexpr int kStages = 5;
+    // pairs give one stage's room to the epilogue, whose stores would otherwise bound short contractions
+    static constexpr int kStages = PAIR ? 4 : 5;
+    static constexpr int kOutBuffers = SWAP ? 0 : (PAIR ? 4 : 2);       // 32-row x 128-byte store buffers an epilogue warp
     // Two accumulators.  At BN = 256 they overlap by 96 of TMEM's columns
     // (the scales need the rest): the epilogue takes those columns into
     // registers first and hands them back at once, so the next tile's MMAs
@@ -229,7 +233,7 @@ struct Geo {
     static constexpr int kQAtoms = BN <= 128 ? 1 : BN / 128;    // 128-row pieces of Q's scales
     static constexpr int kStageScales = round_up(kScalesP, 128) + (kScalesQ > 1024 ? round_up(kScalesQ, 128) : 1024);
     static constexpr int kScalesQAt = round_up(kScalesP, 128);  // where a stage's Q scales start
-    static constexpr int kOutBytes = SWAP ? 0 : 4 * 2 * 4096;   // two 32-row x 128-byte store buffers an epilogue warp
+    static constexpr int kOutBytes = 4 * kOutBuffers * 4096;
     static constexpr int kSmem = kStages * (kStageCodes + kStageScales) + kOutBytes + 1024;
     static constexpr int kQCols = 4 * kQAtoms;                  // TMEM columns of one group's Q scales
     static constexpr int kSfCols = 8 + 2 * kQCols;
@@ -353,109 +357,157 @@ __device__ __forceinline__ void store_swapped(const Mx4GemmArgs& a, const Tile& 
     else store_swapped<N, kBF16>(a, t, lane_row, c0, x);
 }
 
-// An epilogue warp's two buffers of 32 rows x 128 bytes (swizzled as the
-// output's tensor map expects), each stored by TMA in whole lines: direct
-// stores, 32 bytes a lane in 32 different rows, took longer than a main loop
-// of 2,048 (80 us against 62 us for 8192 x 8192 x 2048).
-struct StoreBuffers {
-    uint8_t* base;
-    uint32_t used = 0;
-    bool pending = false;
-    __device__ explicit StoreBuffers(uint8_t* at) : base(at) {}
+__device__ __forceinline__ void store_shared16(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" :: "r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
 
-    // 32 columns c .. c+31 (c a multiple of 32) of the warp's 32 rows, all of
-    // which exist; the map's bounds cut columns behind D's last.  fp32 fills a
-    // buffer with one call, 16-bit outputs with two, in either order: c and
-    // c ^ 32.
-    __device__ __forceinline__ void put(const CUtensorMap& map, const Mx4GemmArgs& a, const Tile& t, int warp, int lane, int c,
-                                        const float (&x)[32])
-    {
-        const bool wide = a.dtype == kF32;
-        uint8_t* buf = base + (used & 1) * 4096;
-        const int at = c & 32 ? 4 : 0;        // first 16-byte chunk of a 16-bit row
-        if (!pending) {
-            // the buffer's store of two before has been read
-            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-            __syncwarp();
-        }
-        uint8_t* row = buf + lane * 128;
-        const int sw = lane & 7;
-        if (wide) {
+// The warp's bulk stores, whichever lanes issued them, have read their buffers.
+__device__ __forceinline__ void stores_read()
+{
+    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
+}
+
+// `bytes` (a multiple of 16) from shared to global memory, both 16-byte aligned.
+__device__ __forceinline__ void bulk_store(void* to, uint32_t from, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\t"
+                 "cp.async.bulk.commit_group;" :: "l"(to), "r"(from), "r"(bytes) : "memory");
+}
+
+// An epilogue warp's 32 rows of a tile from its accumulator (columns acc ..) to
+// D, whose rows start on 32 bytes: through NB buffers of 32 rows x 128 bytes.
+// With PART false all 32 rows exist and a buffer is stored by TMA in whole
+// lines (swizzled as the output's tensor map expects, whose bounds cut columns
+// behind D's last).  With PART true `rows` of them exist, and each of these is
+// a bulk copy of its lane's (D's columns then end on 16 bytes; the buffer's
+// rows are 144 bytes apart against bank conflicts).  chunk(i) is the first of
+// the 32 columns that come i-th; release() is called once the first FIRST of
+// them (three, in registers together) or all (FIRST = 0) are read.  ZERO:
+// zeros instead.
+// Direct stores, 32 bytes a lane in 32 different rows, bounded a product of
+// 2,048 columns (80 us against 64 us for 8,192 x 8,192 x 2,048); rows of a
+// partial tile stored 64 bytes an instruction made eight uneven experts of
+// 2,048 x 2,048 take 38 us where now 28.
+template <int DT, int BN, int FIRST, int NB, bool PART, bool ZERO, typename Chunk, typename Release>
+__device__ __forceinline__ void store_tile(const CUtensorMap& map, const Mx4GemmArgs& a, const Tile& t, uint32_t acc, int warp,
+                                           int lane, int rows, uint32_t buf0, Chunk chunk, Release release)
+{
+    constexpr bool kWide = DT == kF32;                   // a buffer holds 32 columns, else 64: two chunks that come together
+    constexpr int kBuffers = PART ? NB * 4096 / (32 * 144) : NB, kBytes = PART ? 32 * 144 : 4096;
+    const uint32_t row = buf0 + lane * (PART ? 144 : 128);
+    const uint32_t sw = PART ? 0u : static_cast<uint32_t>(lane & 7) << 4;
+    const int d_cols = static_cast<int>(a.d_cols);
+    const int64_t y = t.d_row + (warp & 3) * 32;
+    auto put = [&](int i, const float (&x)[32]) {
+        constexpr int kRound = kWide ? kBuffers : 2 * kBuffers;
+        if (i % kRound == 0) stores_read();
+        const int c = chunk(i), k = kWide ? i % kBuffers : i / 2 % kBuffers;
+        const uint32_t at = row + k * kBytes;
+        if constexpr (kWide) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                *reinterpret_cast<float4*>(row + ((k ^ sw) << 4)) = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+            for (uint32_t j = 0; j < 8; ++j)
+                store_shared16(at + ((j << 4) ^ sw), __float_as_uint(x[4 * j]), __float_as_uint(x[4 * j + 1]),
+                               __float_as_uint(x[4 * j + 2]), __float_as_uint(x[4 * j + 3]));
         } else {
+            const uint32_t half = static_cast<uint32_t>(c & 32) << 1;           // the row's second 64 bytes
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                uint4 v;
-                if (a.dtype == kF16)
-                    v = make_uint4(pack_out<kF16>(x[8 * k], x[8 * k + 1]), pack_out<kF16>(x[8 * k + 2], x[8 * k + 3]),
-                                   pack_out<kF16>(x[8 * k + 4], x[8 * k + 5]), pack_out<kF16>(x[8 * k + 6], x[8 * k + 7]));
-                else
-                    v = make_uint4(pack_out<kBF16>(x[8 * k], x[8 * k + 1]), pack_out<kBF16>(x[8 * k + 2], x[8 * k + 3]),
-                                   pack_out<kBF16>(x[8 * k + 4], x[8 * k + 5]), pack_out<kBF16>(x[8 * k + 6], x[8 * k + 7]));
-                *reinterpret_cast<uint4*>(row + (((at + k) ^ sw) << 4)) = v;
+            for (uint32_t j = 0; j < 4; ++j)
+                store_shared16(at + ((half + (j << 4)) ^ sw), pack_out<DT>(x[8 * j], x[8 * j + 1]),
+                               pack_out<DT>(x[8 * j + 2], x[8 * j + 3]), pack_out<DT>(x[8 * j + 4], x[8 * j + 5]),
+                               pack_out<DT>(x[8 * j + 6], x[8 * j + 7]));
+        }
+        if (kWide || i % 2 == 1) {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            const int col = t.d_col + (kWide ? c : c & ~32);
+            if constexpr (PART) {
+                constexpr int es = kWide ? 4 : 2;
+                const int bytes = min(128, (d_cols - col) * es);
+                if (lane < rows && bytes > 0)
+                    bulk_store(static_cast<uint8_t*>(a.d) + ((y + lane) * a.ldd + col) * es, row + k * kBytes, static_cast<uint32_t>(bytes));
+            } else if (lane == 0 && col < d_cols) {
+                tma_store_2d(&map, col, static_cast<int>(y), buf0 + k * kBytes);
             }
-            pending = !pending;
-            if (pending) return;
         }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        const int col = t.d_col + (wide ? c : c & ~32);
-        if (lane == 0) {
-            if (col < a.d_cols) tma_store_2d(&map, col, static_cast<int>(t.d_row) + (warp & 3) * 32, smem_u32(buf));
-            else asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-        }
-        ++used;
+    };
+    if constexpr (FIRST == 3 && !ZERO) {
+        float x[3][32];
+        tmem_ld(acc + chunk(0), acc + chunk(2), x);
+        release();
+#pragma unroll
+        for (int i = 0; i < 3; ++i) put(i, x[i]);
     }
-    // The same columns where rows are missing, D's rows do not start on 32
-    // bytes, or D is added to: through a buffer, each row as 32 neighbouring
-    // elements of a warp (stored by the lanes that hold the rows, 32 rows an
-    // instruction, 999 x 531 x 1,000 into fp32 took 28 us).
-    template <int DT>
-    __device__ __forceinline__ void put_rows_as(const Mx4GemmArgs& a, const Tile& t, int warp, int lane, int c, const float (&x)[32])
-    {
-        float* buf = reinterpret_cast<float*>(base);
+#pragma unroll 1
+    for (int i = ZERO ? 0 : FIRST; i < BN / 32; ++i) {
+        float x[32] = {};
+        if (!ZERO) tmem_ld(acc + chunk(i), x);
+        put(i, x);
+    }
+    if constexpr (FIRST == 0 && !ZERO) release();
+}
+
+// The same where rows are missing (1 to 32 exist), D's rows do not start on 32
+// bytes, or D is added to: each row as 32 neighbouring elements of the warp
+// (stored by the lanes that hold the rows, 32 rows an instruction, 999 x 531 x
+// 1,000 into fp32 took 28 us; so, 8 us).  From zeros when ZERO.
+template <int DT, int BN, int FIRST, bool ZERO, typename Chunk, typename Release>
+__device__ __forceinline__ void store_rows(const Mx4GemmArgs& a, const Tile& t, uint32_t acc, int warp, int lane, float* buf,
+                                           Chunk chunk, Release release)
+{
+    const int rows = min(32, t.d_rows - (warp & 3) * 32);
+    stores_read();                                       // of earlier tiles
+    auto put = [&](int i, const float (&x)[32]) {
+        const int col = t.d_col + chunk(i) + lane;
+        if (col - lane >= a.d_cols) return;
 #pragma unroll
         for (int k = 0; k < 32; ++k) buf[lane * 32 + (k ^ lane)] = x[k];
         __syncwarp();
-        const int rows = min(32, t.d_rows - (warp & 3) * 32), col = t.d_col + c + lane;
         if (col < a.d_cols) {
             const int64_t at = (t.d_row + (warp & 3) * 32) * a.ldd + col;
-            if (a.accumulate) {
-                for (int r0 = 0; r0 < rows; r0 += 8) {       // eight loads in flight
+            // eight rows' loads before their stores, which the compiler may not move them across
+            for (int r0 = 0; r0 < rows; r0 += 8) {
+                float v[8];
+#pragma unroll
+                for (int r = 0; r < 8; ++r) v[r] = buf[(r0 + r) * 32 + (lane ^ (r0 + r))];
+                if (a.accumulate) {
                     float old[8];
 #pragma unroll
                     for (int r = 0; r < 8; ++r) old[r] = r0 + r < rows ? load_out<DT>(a.d, at + (r0 + r) * a.ldd) : 0.0f;
 #pragma unroll
-                    for (int r = 0; r < 8; ++r)
-                        if (r0 + r < rows)
-                            store_out<DT>(a.d, at + (r0 + r) * a.ldd, __fadd_rn(old[r], buf[(r0 + r) * 32 + (lane ^ (r0 + r))]));
+                    for (int r = 0; r < 8; ++r) v[r] = __fadd_rn(old[r], v[r]);
                 }
-            } else {
-#pragma unroll 8
-                for (int r = 0; r < rows; ++r) store_out<DT>(a.d, at + r * a.ldd, buf[r * 32 + (lane ^ r)]);
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    if (r0 + r < rows) store_out<DT>(a.d, at + (r0 + r) * a.ldd, v[r]);
             }
         }
         __syncwarp();
+    };
+    if constexpr (FIRST == 3 && !ZERO) {
+        float x[3][32];
+        tmem_ld(acc + chunk(0), acc + chunk(2), x);
+        release();
+#pragma unroll
+        for (int i = 0; i < 3; ++i) put(i, x[i]);
     }
-    __device__ __forceinline__ void put_rows(const Mx4GemmArgs& a, const Tile& t, int warp, int lane, int c, const float (&x)[32])
-    {
-        if (t.d_rows <= (warp & 3) * 32 || t.d_col + c >= a.d_cols) return;
-        // stores of earlier tiles may still read the buffers
-        if (used) {
-            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-            __syncwarp();
-        }
-        if (a.dtype == kF32) put_rows_as<kF32>(a, t, warp, lane, c, x);
-        else if (a.dtype == kF16) put_rows_as<kF16>(a, t, warp, lane, c, x);
-        else put_rows_as<kBF16>(a, t, warp, lane, c, x);
+#pragma unroll 1
+    for (int i = ZERO ? 0 : FIRST; i < BN / 32; ++i) {
+        float x[32] = {};
+        if (!ZERO) tmem_ld(acc + chunk(i), x);
+        put(i, x);
     }
-    __device__ __forceinline__ void done(int lane)
-    {
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-    }
-};
+    if constexpr (FIRST == 0 && !ZERO) release();
+}
+
+// f with the output's type as a constant.
+template <typename F> __device__ __forceinline__ void with_dtype(int dtype, F f)
+{
+    if (dtype == kF32) f(std::integral_constant<int, kF32>());
+    else if (dtype == kF16) f(std::integral_constant<int, kF16>());
+    else f(std::integral_constant<int, kBF16>());
+}
 
 // ---------------------------------------------------------------------------
 // The kernel.  Cluster of a.split CTAs along the contraction (1: none, and
@@ -725,64 +777,72 @@ mx4_gemm_kernel(const __grid_constant__ Mx4GemmMaps maps, const Mx4GemmArgs a)
     } else if (warp >= 8) {
         const int lane_row = (warp & 3) * 32 + lane;
         const uint32_t quad = static_cast<uint32_t>(warp & 3) << 21;
-        StoreBuffers out(out_smem + (warp & 3) * 8192);
+        uint8_t* buf = out_smem + (warp & 3) * G::kOutBuffers * 4096;
+        constexpr int kFirst = G::kOverlap / 32;
         uint32_t n = 0;
         for (int t = t0; t < tiles; t += dt) {
             const Tile o = tile_at<BN, SWAP, PAIR>(a, start, first, t, half);
             int lo, hi;
             k_range(o, &lo, &hi);
+            const int rows = o.d_rows - (warp & 3) * 32;         // of this warp (tokens on the lanes' side)
             if (lo < hi) {
                 const int b = n & 1;
                 if (!warp_wait(acc_full(b), (n >> 1) & 1, &abort_flag)) break;
                 fence_after();
                 if (split == 1) {
                     const uint32_t acc = tmem + quad + b * G::kAccStep;
-                    constexpr int kChunk = BN < 32 ? 16 : 32, kFirst = G::kOverlap / 32;
-                    // The shared columns first: the last ones of accumulator 0, the first ones of 1.
-                    // Chunks that share a 64-column store buffer stay neighbours.
-                    auto chunk = [&](int i) {
-                        if constexpr (kFirst == 0) return kChunk * i;
-                        else return 32 * (b ? i : (i < 2 ? 6 + i : (i < 4 ? 7 - i : i - 4)));
+                    auto release = [&] {
+                        fence_before();
+                        __syncwarp();
+                        if (lane == 0) arrive_first(acc_empty(b));
                     };
-                    static_assert(kFirst == 0 || kFirst == 3, "the order above");
-                    const bool whole = !SWAP && a.tma_store && o.d_rows - (warp & 3) * 32 >= 32;
-                    if constexpr (kFirst > 0) {
-                        float x[kFirst][32];
-                        tmem_ld(acc + chunk(0), acc + chunk(2), x);
-                        fence_before();
-                        __syncwarp();
-                        if (lane == 0) arrive_first(acc_empty(b));
-#pragma unroll
-                        for (int i = 0; i < kFirst; ++i) {
-                            if (whole) out.put(maps.d, a, o, warp, lane, chunk(i), x[i]);
-                            else out.put_rows(a, o, warp, lane, chunk(i), x[i]);
-                        }
-                    }
+                    if constexpr (SWAP) {
+                        constexpr int kChunk = BN < 32 ? 16 : 32;
 #pragma unroll 1
-                    for (int i = kFirst; i < BN / kChunk; ++i) {
-                        const int c = chunk(i);
-                        float x[kChunk];
-                        tmem_ld(acc + c, x);
-                        if constexpr (SWAP) store_swapped<kChunk>(a, o, lane_row, c, x);
-                        else if (whole) out.put(maps.d, a, o, warp, lane, c, x);
-                        else out.put_rows(a, o, warp, lane, c, x);
-                    }
-                    if constexpr (kFirst == 0) {
-                        fence_before();
-                        __syncwarp();
-                        if (lane == 0) arrive_first(acc_empty(b));
+                        for (int c = 0; c < BN; c += kChunk) {
+                            float x[kChunk];
+                            tmem_ld(acc + c, x);
+                            store_swapped<kChunk>(a, o, lane_row, c, x);
+                        }
+                        release();
+                    } else if (rows <= 0) {
+                        release();
+                    } else {
+                        // The shared columns first: the last ones of accumulator 0, the first ones of 1.
+                        // Chunks that share a 64-column store buffer stay neighbours.
+                        static_assert(kFirst == 0 || kFirst == 3, "the order here");
+                        auto chunk = [&](int i) {
+                            if constexpr (kFirst == 0) return 32 * i;
+                            else return 32 * (b ? i : (i < 2 ? 6 + i : (i < 4 ? 7 - i : i - 4)));
+                        };
+                        with_dtype(a.dtype, [&](auto dt_) {
+                            constexpr int DT = decltype(dt_)::value;
+                            if (a.tma_store && rows >= 32)
+                                store_tile<DT, BN, kFirst, G::kOutBuffers, false, false>(maps.d, a, o, acc, warp, lane, 32, smem_u32(buf),
+                                                                                  chunk, release);
+                            else if (a.tma_store && a.d_cols * (DT == kF32 ? 4 : 2) % 16 == 0)
+                                store_tile<DT, BN, kFirst, G::kOutBuffers, true, false>(maps.d, a, o, acc, warp, lane, rows, smem_u32(buf),
+                                                                                 chunk, release);
+                            else
+                                store_rows<DT, BN, kFirst, false>(a, o, acc, warp, lane, reinterpret_cast<float*>(buf), chunk, release);
+                        });
                     }
                 }
                 ++n;
-            } else if (!SWAP && !a.accumulate) {         // an empty group's product
-                if constexpr (!SWAP) {
-                    const float zero[32] = {};
-#pragma unroll 1
-                    for (int c = 0; c < BN; c += 32) out.put_rows(a, o, warp, lane, c, zero);
-                }
+            } else if (!SWAP && !a.accumulate && rows > 0) {     // an empty group's product
+                if constexpr (!SWAP)
+                    with_dtype(a.dtype, [&](auto dt_) {
+                        constexpr int DT = decltype(dt_)::value;
+                        auto chunk = [](int i) { return 32 * i; };
+                        if (a.tma_store && rows >= 32)
+                            store_tile<DT, BN, kFirst, G::kOutBuffers, false, true>(maps.d, a, o, 0u, warp, lane, 32, smem_u32(buf),
+                                                                                    chunk, [] {});
+                        else
+                            store_rows<DT, BN, kFirst, true>(a, o, 0u, warp, lane, reinterpret_cast<float*>(buf), chunk, [] {});
+                    });
             }
         }
-        out.done(lane);
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
 
     if (split > 1) {

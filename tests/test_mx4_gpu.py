@@ -166,6 +166,8 @@ def gpu_close(got, a, b):
     y, mag = a @ b.mT, a.abs() @ b.abs().mT
     tol = a.shape[-1] * 2.0 ** -23 * mag
     tol = tol + torch.finfo(got.dtype).eps / 2 * (y.abs() + tol)
+    if got.dtype == torch.float16:
+        tol = tol + 2.0 ** -25            # below 2^-14 fp16 values are 2^-24 apart: half a step, as in product_bound
     assert ((got.double() - y).abs() <= tol).all()
 
 
@@ -192,8 +194,10 @@ def test_matmul_long(mx4, m, n, k):
         assert torch.equal(d, first.to(d.dtype))
 
 
-@pytest.mark.parametrize("groups,tokens,n,k", [(5, 3000, 700, 1500), (40, 1500, 520, 1300), (130, 100, 300, 2048)])
-def test_grouped_long(mx4, groups, tokens, n, k):
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("groups,tokens,n,k", [(5, 3000, 700, 1500), (5, 3000, 528, 1040), (40, 1500, 520, 1300),
+                                               (130, 100, 300, 2048)])
+def test_grouped_long(mx4, groups, tokens, n, k, dtype):
     r = np.random.RandomState(groups)
     share = np.exp(1.5 * r.standard_normal(groups))
     counts = r.multinomial(tokens, share / share.sum()).tolist()
@@ -207,7 +211,11 @@ def test_grouped_long(mx4, groups, tokens, n, k):
     flush = torch.empty(64 << 20, device="cuda")
     for i in range(3):
         flush.normal_(generator=g)
-        y, dw = mx4.matmul_grouped(xq, w, off, torch.float32), mx4.matmul_ragged(dt, xt, off, torch.float32)
+        y, dw = (torch.full(s, 7.0, dtype=DTYPES[dtype], device="cuda") for s in ((tokens + 3, n + 16), (groups * n, k + 16)))
+        mx4.matmul_grouped(xq, w, off, out=y[:tokens, :n])
+        mx4.matmul_ragged(dt, xt, off, out=dw.view(groups, n, k + 16)[..., :k])
+        assert (y[tokens:] == 7).all() and (y[:, n:] == 7).all() and (dw[:, k:] == 7).all()
+        y, dw = y[:tokens, :n], dw.view(groups, n, k + 16)[..., :k]
         at = col = 0
         for e, c in enumerate(counts):
             gpu_close(y[at:at + c], xv[at:at + c], wv[e])
