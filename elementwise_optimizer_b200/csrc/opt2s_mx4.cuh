@@ -127,14 +127,12 @@ template <> struct Src<kF32> {
     __device__ static float element(const uint32_t* w, int i) { return __uint_as_float(w[i]); }
     __device__ static float half(uint32_t w, int) { return __uint_as_float(w); }
     __device__ static uint32_t magnitude(uint32_t bits) { return bits; }
-    __device__ static uint32_t bits(const void* p, int64_t i) { return static_cast<const uint32_t*>(p)[i]; }
 };
 template <> struct Src<kBF16> {
     static constexpr int kPer = 8, kBytes = 2;
     __device__ static float half(uint32_t w, int j) { return __uint_as_float(j ? w & 0xFFFF0000u : w << 16); }
     __device__ static float element(const uint32_t* w, int i) { return half(w[i / 2], i & 1); }
     __device__ static uint32_t magnitude(uint32_t bits) { return bits << 16; }
-    __device__ static uint32_t bits(const void* p, int64_t i) { return static_cast<const uint16_t*>(p)[i]; }
 };
 template <> struct Src<kF16> {
     static constexpr int kPer = 8, kBytes = 2;
@@ -145,7 +143,6 @@ template <> struct Src<kF16> {
     }
     __device__ static float element(const uint32_t* w, int i) { return half(w[i / 2], i & 1); }
     __device__ static uint32_t magnitude(uint32_t bits) { return abs_bits(half(bits, 0)); }
-    __device__ static uint32_t bits(const void* p, int64_t i) { return static_cast<const uint16_t*>(p)[i]; }
 };
 
 // The largest magnitude of words of a 16-bit type, each half on its own.

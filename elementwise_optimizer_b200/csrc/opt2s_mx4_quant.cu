@@ -6,6 +6,8 @@
 // 128 x 128 tile once into shared memory and writes both forms from there.
 // The kernel is bound by memory traffic: 16-bit sources read 2 bytes an
 // element (3 with noise) and write 17/32 byte per form.
+#include <type_traits>
+
 #include "opt2s_mx4.cuh"
 
 namespace opt2s {
@@ -20,6 +22,32 @@ __device__ __forceinline__ void copy16(uint8_t* dst, const void* src, bool in)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
                  :: "r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+
+// A tile of elements of B bytes whose rows do not start on 16 bytes: a warp
+// takes neighbouring elements of a row, four rows in flight.  `place` says
+// where an element goes.
+template <int B, int COLS, typename Place>
+__device__ __forceinline__ void load_elements(const uint8_t* x, int64_t pitch, int rows, int cols, int tid, Place place)
+{
+    using T = std::conditional_t<B == 4, uint32_t, std::conditional_t<B == 2, uint16_t, uint8_t>>;
+    constexpr int kAcross = COLS / 32, kRows = 4;
+    const T* p = reinterpret_cast<const T*>(x);
+    const int lane = tid & 31;
+    for (int r0 = (tid >> 5) * kRows; r0 < kTileRows; r0 += kQuantThreads / 32 * kRows) {
+        T v[kRows][kAcross];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+#pragma unroll
+            for (int k = 0; k < kAcross; ++k) {
+                const int e = k * 32 + lane;
+                v[r][k] = r0 + r < rows && e < cols ? p[(r0 + r) * pitch + e] : T{0};
+            }
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+#pragma unroll
+            for (int k = 0; k < kAcross; ++k) *reinterpret_cast<T*>(place(r0 + r, k * 32 + lane)) = v[r][k];
+    }
 }
 
 // Starts the load of one tile of the source (zeros outside it) into shared
@@ -43,16 +71,9 @@ __device__ __forceinline__ void load_tile(const Mx4QuantArgs& a, int64_t row0, i
                 copy16(tile + tile_chunk<DT, kTileCols>(r, c), in ? p + r * pitch : static_cast<const uint8_t*>(a.x), in);
             }
         } else {
-            for (int r = tid / kChunks; r < kTileRows; r += kStep) {
-                uint32_t w[4] = {0, 0, 0, 0};
-                if (r < rows) {
-#pragma unroll
-                    for (int k = 0; k < P; ++k)
-                        if (at + k < cols)
-                            w[k * S::kBytes / 4] |= S::bits(x, r * a.row_stride + at + k) << (S::kBytes == 2 ? 16 * (k & 1) : 0);
-                }
-                *reinterpret_cast<uint4*>(tile + tile_chunk<DT, kTileCols>(r, c)) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+            load_elements<S::kBytes, kTileCols>(x, a.row_stride, rows, cols, tid, [&](int r, int e) {
+                return tile + tile_chunk<DT, kTileCols>(r, e / P) + e % P * S::kBytes;
+            });
         }
     }
     if (NOISE) {
@@ -65,15 +86,8 @@ __device__ __forceinline__ void load_tile(const Mx4QuantArgs& a, int64_t row0, i
                 copy16(noise + noise_chunk<kTileCols>(r, c), in ? n + r * a.cols + at : a.noise, in);
             }
         } else {
-            for (int r = tid / 8; r < kTileRows; r += kQuantThreads / 8) {
-                uint32_t w[4] = {0, 0, 0, 0};
-                if (r < rows) {
-#pragma unroll
-                    for (int k = 0; k < 16; ++k)
-                        if (at + k < cols) w[k / 4] |= static_cast<uint32_t>(n[r * a.cols + at + k]) << (8 * (k & 3));
-                }
-                *reinterpret_cast<uint4*>(noise + noise_chunk<kTileCols>(r, c)) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+            load_elements<1, kTileCols>(n, a.cols, rows, cols, tid,
+                                        [&](int r, int e) { return noise + noise_chunk<kTileCols>(r, e / 16) + e % 16; });
         }
     }
 }
