@@ -15,6 +15,15 @@
 // scales are contiguous whatever row it starts at: groups of rows that begin
 // anywhere (experts) need no copy and no padding.
 //
+// What bounds it, at 8,192 x 8,192 x 2,048 (65 us: 4.2 PFLOP/s, 2.5 times the
+// library's measured bf16 rate): a pair's stage takes 730 cycles where its
+// MMAs take 512, the copies of its scales to TMEM about 40 each (six, in the
+// same pipe), and between two tiles the pipe stands still for about 900 cycles
+// (the accumulators' hand-over).  8,192^3 takes 190 us (5.8 PFLOP/s) from a
+// cool chip and 236 us (4.7) for seconds on end, where the power limit lowers
+// the clock.  The contraction's loads arrive about 1,000 cycles before they are
+// needed.
+//
 // Every wait is bounded: a wait that runs out raises the CTA's abort flag and
 // the library's error flag (opt2s_mx4_errors), and the CTA drains its copies,
 // frees its TMEM and returns.
@@ -387,7 +396,7 @@ __device__ __forceinline__ void bulk_store(void* to, uint32_t from, uint32_t byt
 // them (three, in registers together) or all (FIRST = 0) are read.  ZERO:
 // zeros instead.
 // Direct stores, 32 bytes a lane in 32 different rows, bounded a product of
-// 2,048 columns (80 us against 64 us for 8,192 x 8,192 x 2,048); rows of a
+// 2,048 columns (80 us against 65 us for 8,192 x 8,192 x 2,048); rows of a
 // partial tile stored 64 bytes an instruction made eight uneven experts of
 // 2,048 x 2,048 take 38 us where now 28.
 template <int DT, int BN, int FIRST, int NB, bool PART, bool ZERO, typename Chunk, typename Release>
@@ -1030,9 +1039,10 @@ cudaError_t launch_mx4_gemm(Mx4GemmArgs a, const Mx4GemmOperands& op, cudaStream
     a.split = 1;
     // 256 x 256 tiles by pairs of CTAs, or 128 x 128 tiles by single ones: the
     // fewer rounds of tiles, weighted by what a 256-element stage of each takes
-    // (0.42 us for a pair's, 0.30 us for a single's, both bound by the loads),
-    // decide.  256 x 8,192 x 2,048 takes 18 us in pairs and 14 us in singles,
-    // 8,192 x 8,192 x 2,048 68 us in pairs and 85 us in singles.
+    // (0.42 us for a pair's, 0.30 us for a single's), decide.  Measured, pairs
+    // and singles: 256 x 8,192 x 2,048 8.4 and 7.1 us, 512 x 8,192 x 2,048 9.6
+    // and 11.0, 4,096 x 2,048 x 8,192 32.6 and 46.2, 8,192 x 8,192 x 2,048 65
+    // and 92, 999 x 531 x 1,000 14.9 and 9.3.
     auto pairs_win = [&](int64_t groups, int64_t rows, int64_t cols) {
         auto rounds = [&](int64_t tile, int64_t at_once) {
             const int64_t tiles = groups * ((rows + tile - 1) / tile) * ((cols + tile - 1) / tile);

@@ -4,8 +4,13 @@
 // (the contraction of the forward product) and in blocks down its columns,
 // transposed (the contraction of the backward products).  One CTA reads a
 // 128 x 128 tile once into shared memory and writes both forms from there.
-// The kernel is bound by memory traffic: 16-bit sources read 2 bytes an
-// element (3 with noise) and write 17/32 byte per form.
+// A 4,096 x 8,192 bf16 source takes 24 us (4.2 TB/s of its 103 MB; 16 us at
+// the measured copy rate) and 43 us with noise (3.2 TB/s of 136 MB; 21 us):
+// instructions bound it, 15 an element and 34 with noise (62 % of the issue
+// slots, the ALU pipe 80 % busy with noise); fp32 reaches 5.8 TB/s.  Loads by
+// cp.async, all of a tile's in flight at once; a persistent form that loaded
+// the next tile meanwhile was slower (27 and 55 us), and other numbers of
+// resident CTAs were no faster.
 #include <type_traits>
 
 #include "opt2s_mx4.cuh"
@@ -163,13 +168,14 @@ template <int DT> __device__ __forceinline__ uint32_t pack2(float lo, float hi)
 
 // grid: x = groups of 4 rows, y = 4,096-column parts, z = slabs.  A thread
 // takes 16 elements (8 bytes of codes, half a block) of each row; all loads
-// come first, and 16-bit outputs are stored 32 bytes a thread.  Outputs whose
-// rows do not start on 32 bytes take two elements a thread and step instead,
+// come first, and 16-bit outputs are stored 32 bytes a thread: 4,096 x 8,192
+// to bf16 takes 12 us (7.1 TB/s).  Outputs whose rows do not start on 32 bytes
+// (VEC false) take two elements a thread and step and one row a CTA instead,
 // so that a warp still stores neighbouring elements.
-template <int DT>
+template <int DT, bool VEC>
 __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const Mx4DequantArgs a)
 {
-    constexpr int kRows = 4, kPart = 4096;
+    constexpr int kRows = VEC ? 4 : 1, kPart = 4096;
     const int64_t cp = (a.cols + 127) / 128 * 128, rp = (a.rows + 3) / 4 * 4;
     const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kRows, slab = blockIdx.z, col0 = static_cast<int64_t>(blockIdx.y) * kPart;
     const int rows = static_cast<int>(min(static_cast<int64_t>(kRows), a.rows - row0));
@@ -177,7 +183,7 @@ __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const Mx4DequantArg
     const uint8_t* scales = a.scales + (slab * rp + row0) * 4;
     const int64_t group = a.slabs * rp * 4;           // bytes of scales per 128-column group
     const int64_t out0 = (slab * a.rows + row0) * a.cols;
-    if (a.vec) {
+    if constexpr (VEC) {
         const int64_t c0 = col0 + threadIdx.x * 16;
         if (c0 >= a.cols) return;
         uint2 w[kRows];
@@ -216,25 +222,23 @@ __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const Mx4DequantArg
         }
         return;
     }
-    for (int r = 0; r < rows; ++r) {
 #pragma unroll
-        for (int it = 0; it < kPart / 512; ++it) {
-            const int64_t c0 = col0 + (it * 256 + threadIdx.x) * 2;
-            if (c0 >= a.cols) break;
-            const float2 f = decode2(codes[r * (cp / 2) + c0 / 2]);
-            const float scale = scale_value(scales[(c0 >> 7) * group + r * 4 + ((c0 >> 5) & 3)]);
-            const float x0 = __fmul_rn(f.x, scale), x1 = __fmul_rn(f.y, scale);
-            const int64_t at = out0 + r * a.cols + c0;
-            if (DT == kF32) {
-                float* d = static_cast<float*>(a.out) + at;
-                d[0] = x0;
-                if (c0 + 1 < a.cols) d[1] = x1;
-            } else {
-                uint16_t* d = static_cast<uint16_t*>(a.out) + at;
-                const uint32_t h = pack2<DT>(x0, x1);
-                d[0] = static_cast<uint16_t>(h);
-                if (c0 + 1 < a.cols) d[1] = static_cast<uint16_t>(h >> 16);
-            }
+    for (int it = 0; it < kPart / 512; ++it) {
+        const int64_t c0 = col0 + (it * 256 + threadIdx.x) * 2;
+        if (c0 >= a.cols) break;
+        const float2 f = decode2(codes[c0 / 2]);
+        const float scale = scale_value(scales[(c0 >> 7) * group + ((c0 >> 5) & 3)]);
+        const float x0 = __fmul_rn(f.x, scale), x1 = __fmul_rn(f.y, scale);
+        const int64_t at = out0 + c0;
+        if (DT == kF32) {
+            float* d = static_cast<float*>(a.out) + at;
+            d[0] = x0;
+            if (c0 + 1 < a.cols) d[1] = x1;
+        } else {
+            uint16_t* d = static_cast<uint16_t*>(a.out) + at;
+            const uint32_t h = pack2<DT>(x0, x1);
+            d[0] = static_cast<uint16_t>(h);
+            if (c0 + 1 < a.cols) d[1] = static_cast<uint16_t>(h >> 16);
         }
     }
 }
@@ -270,11 +274,15 @@ cudaError_t launch_mx4_quantize(const Mx4QuantArgs& a, int dtype, int64_t row_ti
 
 cudaError_t launch_mx4_dequantize(const Mx4DequantArgs& a, int dtype, cudaStream_t stream)
 {
-    const dim3 grid(static_cast<unsigned>((a.rows + 3) / 4), static_cast<unsigned>((a.cols + 4095) / 4096),
+    const dim3 grid(static_cast<unsigned>(a.vec ? (a.rows + 3) / 4 : a.rows), static_cast<unsigned>((a.cols + 4095) / 4096),
                     static_cast<unsigned>(a.slabs));
-    if (dtype == kF32) mx4_dequantize_kernel<kF32><<<grid, 256, 0, stream>>>(a);
-    else if (dtype == kF16) mx4_dequantize_kernel<kF16><<<grid, 256, 0, stream>>>(a);
-    else mx4_dequantize_kernel<kBF16><<<grid, 256, 0, stream>>>(a);
+    auto go = [&](auto* wide, auto* any) {
+        if (a.vec) wide<<<grid, 256, 0, stream>>>(a);
+        else any<<<grid, 256, 0, stream>>>(a);
+    };
+    if (dtype == kF32) go(mx4_dequantize_kernel<kF32, true>, mx4_dequantize_kernel<kF32, false>);
+    else if (dtype == kF16) go(mx4_dequantize_kernel<kF16, true>, mx4_dequantize_kernel<kF16, false>);
+    else go(mx4_dequantize_kernel<kBF16, true>, mx4_dequantize_kernel<kBF16, false>);
     return cudaGetLastError();
 }
 

@@ -9,7 +9,10 @@
 // in shared memory as they are stored, and encodes both forms from there.
 // Tensors without copies are stepped in the same launch, 8,192 elements a
 // CTA, a warp on each of eight chunks.  Bound by memory traffic, as the plain
-// step is.
+// step is: four tensors of 2,048 x 8,192 take 338 us with AdEMAMix over bf16
+// (6.2 TB/s of 30 + 17/16 bytes an element; 315 us without copies) and 311 us
+// with Adam over fp32 (6.3 TB/s); Adam over bf16, 283 us (5.5 TB/s; 231 us
+// without), has the least traffic to hide the encoding behind.
 //
 // The records travel as kernel arguments (up to 256 a launch): no table in
 // device memory, nothing kept between calls, and a captured launch holds all

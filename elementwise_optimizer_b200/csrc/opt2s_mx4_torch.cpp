@@ -2,10 +2,11 @@
 // (elementwise_optimizer_b200/mx4.py), part of the marshalling extension:
 // checks of tensors, allocation of outputs, the calls of the C ABI on the
 // tensors' device and current stream, and the layers' autograd function.  A
-// layer's forward and backward make six library calls; marshalled in Python
-// they cost 250 us of host time, here about a tenth of it.  No arithmetic is
-// here.  The library's entry points are handed over by address
-// (mx4_set_library), so the extension does not link against it.
+// layer's forward and backward make six library calls: 256 us of host time
+// marshalled in Python, 102 us here, of which torch's engine takes 80 (a
+// forward alone takes 20).  No arithmetic is here.  The library's entry points
+// are handed over by address (mx4_set_library), so the extension does not link
+// against it.
 #include <torch/extension.h>
 
 #include <c10/cuda/CUDAGuard.h>
