@@ -430,6 +430,15 @@ def make_hyper(algo: str = "adam", lr: float = 1e-3, beta1: float = 0.9,
                  int(bool(skip_zeros)))
 
 
+def bump_versions(tensors) -> None:
+    """Tell autograd that the library has written these tensors (those made
+    in inference mode have no version)."""
+    import torch
+    tensors = [t for t in tensors if not t.is_inference()]
+    if tensors:
+        torch.autograd.graph.increment_version(tensors)
+
+
 def _current_stream_fast():
     """Raw handle of torch's current stream on the current device.  Building
     a torch.cuda.Stream object costs microseconds per call, so the private

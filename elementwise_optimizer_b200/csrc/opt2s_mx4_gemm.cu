@@ -193,10 +193,31 @@ __device__ __forceinline__ void tmem_ld(uint32_t at, float (&x)[32])
 // 64 columns at `at` and 32 at `more`, one wait.
 __device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t more, float (&x)[3][32])
 {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%96];\n\t"
-                 "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, %80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95}, [%97];\n\t"
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+                 "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+                 "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+                 "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%96];\n\t"
+                 "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+                 "%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, "
+                 "%80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95}, [%97];\n\t"
                  "tcgen05.wait::ld.sync.aligned;"
-                 : "=f"(x[0][0]), "=f"(x[0][1]), "=f"(x[0][2]), "=f"(x[0][3]), "=f"(x[0][4]), "=f"(x[0][5]), "=f"(x[0][6]), "=f"(x[0][7]), "=f"(x[0][8]), "=f"(x[0][9]), "=f"(x[0][10]), "=f"(x[0][11]), "=f"(x[0][12]), "=f"(x[0][13]), "=f"(x[0][14]), "=f"(x[0][15]), "=f"(x[0][16]), "=f"(x[0][17]), "=f"(x[0][18]), "=f"(x[0][19]), "=f"(x[0][20]), "=f"(x[0][21]), "=f"(x[0][22]), "=f"(x[0][23]), "=f"(x[0][24]), "=f"(x[0][25]), "=f"(x[0][26]), "=f"(x[0][27]), "=f"(x[0][28]), "=f"(x[0][29]), "=f"(x[0][30]), "=f"(x[0][31]), "=f"(x[1][0]), "=f"(x[1][1]), "=f"(x[1][2]), "=f"(x[1][3]), "=f"(x[1][4]), "=f"(x[1][5]), "=f"(x[1][6]), "=f"(x[1][7]), "=f"(x[1][8]), "=f"(x[1][9]), "=f"(x[1][10]), "=f"(x[1][11]), "=f"(x[1][12]), "=f"(x[1][13]), "=f"(x[1][14]), "=f"(x[1][15]), "=f"(x[1][16]), "=f"(x[1][17]), "=f"(x[1][18]), "=f"(x[1][19]), "=f"(x[1][20]), "=f"(x[1][21]), "=f"(x[1][22]), "=f"(x[1][23]), "=f"(x[1][24]), "=f"(x[1][25]), "=f"(x[1][26]), "=f"(x[1][27]), "=f"(x[1][28]), "=f"(x[1][29]), "=f"(x[1][30]), "=f"(x[1][31]), "=f"(x[2][0]), "=f"(x[2][1]), "=f"(x[2][2]), "=f"(x[2][3]), "=f"(x[2][4]), "=f"(x[2][5]), "=f"(x[2][6]), "=f"(x[2][7]), "=f"(x[2][8]), "=f"(x[2][9]), "=f"(x[2][10]), "=f"(x[2][11]), "=f"(x[2][12]), "=f"(x[2][13]), "=f"(x[2][14]), "=f"(x[2][15]), "=f"(x[2][16]), "=f"(x[2][17]), "=f"(x[2][18]), "=f"(x[2][19]), "=f"(x[2][20]), "=f"(x[2][21]), "=f"(x[2][22]), "=f"(x[2][23]), "=f"(x[2][24]), "=f"(x[2][25]), "=f"(x[2][26]), "=f"(x[2][27]), "=f"(x[2][28]), "=f"(x[2][29]), "=f"(x[2][30]), "=f"(x[2][31])
+                 : "=f"(x[0][0]), "=f"(x[0][1]), "=f"(x[0][2]), "=f"(x[0][3]), "=f"(x[0][4]), "=f"(x[0][5]),
+                   "=f"(x[0][6]), "=f"(x[0][7]), "=f"(x[0][8]), "=f"(x[0][9]), "=f"(x[0][10]), "=f"(x[0][11]),
+                   "=f"(x[0][12]), "=f"(x[0][13]), "=f"(x[0][14]), "=f"(x[0][15]), "=f"(x[0][16]), "=f"(x[0][17]),
+                   "=f"(x[0][18]), "=f"(x[0][19]), "=f"(x[0][20]), "=f"(x[0][21]), "=f"(x[0][22]), "=f"(x[0][23]),
+                   "=f"(x[0][24]), "=f"(x[0][25]), "=f"(x[0][26]), "=f"(x[0][27]), "=f"(x[0][28]), "=f"(x[0][29]),
+                   "=f"(x[0][30]), "=f"(x[0][31]), "=f"(x[1][0]), "=f"(x[1][1]), "=f"(x[1][2]), "=f"(x[1][3]),
+                   "=f"(x[1][4]), "=f"(x[1][5]), "=f"(x[1][6]), "=f"(x[1][7]), "=f"(x[1][8]), "=f"(x[1][9]),
+                   "=f"(x[1][10]), "=f"(x[1][11]), "=f"(x[1][12]), "=f"(x[1][13]), "=f"(x[1][14]), "=f"(x[1][15]),
+                   "=f"(x[1][16]), "=f"(x[1][17]), "=f"(x[1][18]), "=f"(x[1][19]), "=f"(x[1][20]), "=f"(x[1][21]),
+                   "=f"(x[1][22]), "=f"(x[1][23]), "=f"(x[1][24]), "=f"(x[1][25]), "=f"(x[1][26]), "=f"(x[1][27]),
+                   "=f"(x[1][28]), "=f"(x[1][29]), "=f"(x[1][30]), "=f"(x[1][31]), "=f"(x[2][0]), "=f"(x[2][1]),
+                   "=f"(x[2][2]), "=f"(x[2][3]), "=f"(x[2][4]), "=f"(x[2][5]), "=f"(x[2][6]), "=f"(x[2][7]),
+                   "=f"(x[2][8]), "=f"(x[2][9]), "=f"(x[2][10]), "=f"(x[2][11]), "=f"(x[2][12]), "=f"(x[2][13]),
+                   "=f"(x[2][14]), "=f"(x[2][15]), "=f"(x[2][16]), "=f"(x[2][17]), "=f"(x[2][18]), "=f"(x[2][19]),
+                   "=f"(x[2][20]), "=f"(x[2][21]), "=f"(x[2][22]), "=f"(x[2][23]), "=f"(x[2][24]), "=f"(x[2][25]),
+                   "=f"(x[2][26]), "=f"(x[2][27]), "=f"(x[2][28]), "=f"(x[2][29]), "=f"(x[2][30]), "=f"(x[2][31])
                  : "r"(at), "r"(more) : "memory");
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }

@@ -224,6 +224,7 @@ Tensor product(const opt2s_mx4& a, const opt2s_mx4& b, const at::Device& device,
         else if (fits && ragged && groups > 1) ldd = d.stride(0);
         fits = fits && ldd >= b.rows && (n < 3 || groups <= 1 || a.rows == 0 || d.stride(0) == a.rows * ldd);
         TORCH_CHECK_VALUE(fits, message("out must be ", at::IntArrayRef(shape), " with contiguous, evenly spaced rows on ", device));
+        if (!d.is_inference()) d.unsafeGetTensorImpl()->bump_version();       // autograd sees the write
     } else {
         TORCH_CHECK_VALUE(!accumulate, "accumulate needs the tensor to add to (out)");
         d = at::empty(shape, at::TensorOptions().dtype(dtype).device(device));

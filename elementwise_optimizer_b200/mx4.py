@@ -151,7 +151,7 @@ def quantize_pair(x: torch.Tensor, noise: torch.Tensor | None = None, offsets: t
     oq, ot = (None, None) if out is None else (_fields(out[0]), _fields(out[1]))
     q, t = _extension().mx4_quantize(x, noise, offsets, True, True, oq, ot)
     if out is not None:
-        torch.autograd.graph.increment_version([m.codes for m in out])
+        B.bump_versions([m.codes for m in out])
         return tuple(out)
     return MX4Tensor._made(q, x.dim() == 3), MX4Tensor._made(t, x.dim() == 3)
 

@@ -436,8 +436,9 @@ int opt2s_8bit_state_bits(int64_t numel, int64_t min_8bit_size);
  *   scales  [cols_p / 128][slabs * rows_p][4] bytes, rows_p = rows rounded up
  *           to 4: the four blocks of a row in one 128-column group together,
  *           so that any range of rows is contiguous
- * Both pointers are DEVICE memory owned by the caller, 16-byte aligned.
- * cols >= 1; rows may be 0.  The calls below keep nothing between calls,
+ * Both pointers are DEVICE memory owned by the caller, 16-byte aligned.  The
+ * scale bytes of blocks behind cols count too: the calls below write 0, and
+ * none may be 255 (0 * NaN).  cols >= 1; rows may be 0.  The calls below keep nothing between calls,
  * allocate nothing and may be captured in a CUDA graph.
  */
 #define OPT2S_MX4_BLOCK 32
@@ -481,6 +482,7 @@ typedef struct {
  * up to 128), and qt->cols must be rows rounded up to 128, plus
  * 128 * groups; the columns behind a group are codes and scales 0.  Offsets
  * out of range or order are clamped to the rows and to be non-decreasing.
+ * More than 65,535 row tiles of 128 (or slabs) are OPT2S_ERR_TOO_LARGE.
  */
 int opt2s_mx4_quantize(const opt2s_mx4_source *src, const opt2s_mx4 *q, const opt2s_mx4 *qt,
                        const int32_t *offsets, int32_t groups, cudaStream_t stream);

@@ -506,6 +506,52 @@ def test_refusals(mx4):
         torch.autograd.grad(y, xg, torch.ones_like(y).requires_grad_(), create_graph=True)
 
 
+def test_as_many_groups_as_there_may_be(mx4):
+    r = np.random.RandomState(3)
+    counts = r.multinomial(700, np.full(1024, 1 / 1024)).tolist()
+    x, w, dy = mixed((700, 64), torch.float32, 201, 0.25), mixed((1024, 16, 64), torch.float32, 202, 0.25), \
+        mixed((700, 16), torch.float32, 203, 0.25)
+    off = offsets_of(counts)
+    x.requires_grad_()
+    w.requires_grad_()
+    y = mx4.linear_grouped(x, w, off)
+    dx, dw = torch.autograd.grad(y, (x, w), dy)
+    xv, wv, dv, wt = round_ref(x), round_ref(w), round_ref(dy), turned_ref(w)
+    at = 0
+    for e, c in enumerate(counts):
+        s = slice(at, at + c)
+        at += c
+        close(y[s], *product_bound(xv[s], wv[e], torch.float32))
+        close(dx[s], *product_bound(dv[s], wt[e], torch.float32))
+        if c and e % 16 == 0:
+            close(dw[e], *product_bound(turned_ref(dy[s]), turned_ref(x[s]), torch.float32))
+        assert c or not dw[e].any()
+
+
+def test_inference_mode_and_a_graph_used_twice(mx4):
+    x, w = mixed((9, 96), torch.float32, 211), mixed((40, 96), torch.float32, 212)
+    want = mx4.linear(x, w)
+    with torch.inference_mode():
+        pair = mx4.quantize_pair(w)
+        assert torch.equal(mx4.linear(x, w), want) and torch.equal(mx4.linear(x, w, copies=pair), want)
+        assert torch.equal(mx4.project(x, pair[0]), want)
+        mx4.quantize_pair(w, out=pair)
+        mx4.matmul(mx4.quantize(x), pair[0], out=torch.empty(9, 40, device="cuda"))
+    d = torch.empty(9, 40, device="cuda")
+    before = d._version
+    mx4.matmul(mx4.quantize(x), pair[0], out=d)
+    assert d._version > before
+    xg = x.clone().requires_grad_()
+    y = mx4.linear(xg, w)
+    a, = torch.autograd.grad(y, xg, torch.ones_like(y), retain_graph=True)
+    b, = torch.autograd.grad(y, xg, torch.ones_like(y))
+    assert torch.equal(a, b)
+    # checkpointing runs the forward again
+    from torch.utils.checkpoint import checkpoint
+    c, = torch.autograd.grad(checkpoint(lambda t: mx4.linear(t, w), xg, use_reentrant=False), xg, torch.ones_like(y))
+    assert torch.equal(a, c)
+
+
 @pytest.mark.parametrize("need", [(True, True), (True, False), (False, True)])
 def test_empty_batch_of_experts(mx4, need):
     x = torch.empty(0, 96, device="cuda", requires_grad=need[0])
