@@ -71,24 +71,26 @@ __device__ __forceinline__ uint32_t encode8(float x0, float x1, float x2, float 
     return r;
 }
 
-// Stochastic rounding of a scaled element with the byte r: code c or c + 1,
-// the upper one when |x| lies more than (r + 0.5)/256 of the way from c's
-// magnitude to the next.  Returned in the top byte; `flipped` holds the
-// complements of four random bytes, `j` says which one is this element's.
+// Stochastic rounding of a scaled element (|x| < 8) with the byte r: code c or
+// c + 1, the upper one when |x| lies more than (r + 0.5)/256 of the way from
+// c's magnitude to the next.  The complement of the code is the top byte of the
+// result (8 for what pack_noise saturates to 7); `noise` holds four random
+// bytes, `j` says which one is this element's.
 //
-// With a = min(|x|, 6), y = a + max(a, 1) is 1 + a below 1 and 2 a from there
-// on: its exponent and first mantissa bit count the codes, and the other 22
-// bits are the way to the next.  Shifted left by two, the code (plus 254)
-// fills the top byte and the way the 24 bits under it, and the comparison is
-// the carry of adding 2^24 - 1 - 256^2 r - 2^15.  The sum 1 + a is rounded up,
-// which cannot take the way past a threshold (a multiple of 2^13 units of the
-// last bit) that it had not passed, so the comparison is exact for every x.
-__device__ __forceinline__ uint32_t noise_code(float x, uint32_t flipped, int j)
+// With a = |x|, y = a + max(a, 1) is 1 + a below 1 and 2 a from there on: its
+// exponent and first mantissa bit count the codes, and the other 22 bits are
+// the way to the next.  Shifted left by two, the code (plus 254) fills the top
+// byte and the way the 24 bits under it, and the comparison is the carry of
+// adding 2^24 - 1 - 256^2 r - 2^15.  The complement of that sum is one multiply
+// and add with the random byte as it is.  The sum 1 + a is rounded up, which
+// cannot take the way past a threshold (a multiple of 2^13 units of the last
+// bit) that it had not passed, so the comparison is exact for every x.
+__device__ __forceinline__ uint32_t noise_code(float x, uint32_t noise, int j)
 {
-    const float a = fminf(fabsf(x), 6.0f);
+    const float a = fabsf(x);
     const float y = __fadd_ru(a, fmaxf(a, 1.0f));
-    const uint32_t add = __byte_perm(flipped, 0x00027FFFu, 0x6054u | static_cast<uint32_t>(j) << 8);
-    return (__float_as_uint(y) << 2) + add;
+    const uint32_t c = __byte_perm(noise, 0x00FD8000u, 0x6054u | static_cast<uint32_t>(j) << 8);
+    return c - 4u * __float_as_uint(y);
 }
 
 // The top bytes of four words as one word.
@@ -97,13 +99,18 @@ __device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c
     return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
 }
 
-// Eight codes in a word from noise_code's results for x[0..7], signs added.
-__device__ __forceinline__ uint32_t pack_noise(const uint32_t (&t)[8], const float (&x)[8])
+// The signs of eight elements: the top bits of `even`'s bytes are those of
+// elements 0, 2, 4 and 6, of `odd`'s those of 1, 3, 5 and 7.
+struct Signs { uint32_t even, odd; };
+
+// Eight codes in a word from noise_code's results and the signs.
+__device__ __forceinline__ uint32_t pack_noise(const uint32_t (&t)[8], Signs s)
 {
-    const uint32_t even = top_bytes(t[0], t[2], t[4], t[6]), odd = top_bytes(t[1], t[3], t[5], t[7]);
-    const uint32_t se = top_bytes(__float_as_uint(x[0]), __float_as_uint(x[2]), __float_as_uint(x[4]), __float_as_uint(x[6]));
-    const uint32_t so = top_bytes(__float_as_uint(x[1]), __float_as_uint(x[3]), __float_as_uint(x[5]), __float_as_uint(x[7]));
-    return even + (odd << 4) | (se & 0x80808080u) >> 4 | (so & 0x80808080u);
+    const uint32_t even = top_bytes(t[0], t[2], t[4], t[6]), odd = top_bytes(t[1], t[3], t[5], t[7]) << 4;
+    uint32_t w = ~((even & 0x0F0F0F0Fu) | (odd & 0xF0F0F0F0u));
+    w -= w >> 3 & 0x11111111u;                      // 8 to 7
+    const uint32_t sign = (s.even >> 4 & 0x0F0F0F0Fu) | (s.odd & 0xF0F0F0F0u);
+    return (w & 0x77777777u) | (sign & 0x88888888u);
 }
 
 // The two values of a byte of codes.
@@ -120,21 +127,41 @@ __device__ __forceinline__ float2 decode2(uint32_t byte)
 
 // Storage traits of a 4-bit kernel's source: kPer elements in a 16-byte
 // chunk; element i of a run of words; for the 16-bit types one half of a
-// word, and the fp32 bits of a magnitude.
+// word; the fp32 bits of a magnitude; the signs of eight elements.
 template <int DT> struct Src;
 template <> struct Src<kF32> {
     static constexpr int kPer = 4, kBytes = 4;
     __device__ static float element(const uint32_t* w, int i) { return __uint_as_float(w[i]); }
     __device__ static float half(uint32_t w, int) { return __uint_as_float(w); }
     __device__ static uint32_t magnitude(uint32_t bits) { return bits; }
+    __device__ static Signs signs(const uint32_t* w)
+    {
+        return {top_bytes(w[0], w[2], w[4], w[6]), top_bytes(w[1], w[3], w[5], w[7])};
+    }
+    __device__ static Signs signs_down(const uint32_t* w, int) { return signs(w); }
 };
-template <> struct Src<kBF16> {
+struct Halves {
+    // eight elements in four words
+    __device__ static Signs signs(const uint32_t* w)
+    {
+        const uint32_t a = __byte_perm(w[0], w[1], 0x7531), b = __byte_perm(w[2], w[3], 0x7531);
+        return {__byte_perm(a, b, 0x6420), __byte_perm(a, b, 0x7531)};
+    }
+    // half j of eight words (both halves share the first permutes)
+    __device__ static Signs signs_down(const uint32_t* w, int j)
+    {
+        const uint32_t pick = j ? 0x7531 : 0x6420;
+        return {__byte_perm(__byte_perm(w[0], w[2], 0x7531), __byte_perm(w[4], w[6], 0x7531), pick),
+                __byte_perm(__byte_perm(w[1], w[3], 0x7531), __byte_perm(w[5], w[7], 0x7531), pick)};
+    }
+};
+template <> struct Src<kBF16> : Halves {
     static constexpr int kPer = 8, kBytes = 2;
     __device__ static float half(uint32_t w, int j) { return __uint_as_float(j ? w & 0xFFFF0000u : w << 16); }
     __device__ static float element(const uint32_t* w, int i) { return half(w[i / 2], i & 1); }
     __device__ static uint32_t magnitude(uint32_t bits) { return bits << 16; }
 };
-template <> struct Src<kF16> {
+template <> struct Src<kF16> : Halves {
     static constexpr int kPer = 8, kBytes = 2;
     __device__ static float half(uint32_t w, int j)
     {
@@ -148,10 +175,10 @@ template <> struct Src<kF16> {
 // The largest magnitude of words of a 16-bit type, each half on its own.
 __device__ __forceinline__ uint32_t amax_halves(uint32_t amax, uint32_t w) { return __vmaxu2(amax, w & 0x7FFF7FFFu); }
 
-// One word of a block's codes: eight elements x times 2^-e.  flipped(i) and
-// at(i) give element i's random byte as noise_code takes it.
-template <bool NOISE, typename Get, typename Flipped, typename At>
-__device__ __forceinline__ uint32_t encode_word(uint32_t scale, float inv, Get get, Flipped flipped, At at)
+// One word of a block's codes: eight elements x times 2^-e.  noise(i) and
+// at(i) give element i's random byte as noise_code takes it, signs() theirs.
+template <bool NOISE, typename Get, typename Noise, typename At, typename SignsOf>
+__device__ __forceinline__ uint32_t encode_word(uint32_t scale, float inv, Get get, Noise noise, At at, SignsOf signs)
 {
     float x[8];
 #pragma unroll
@@ -160,8 +187,8 @@ __device__ __forceinline__ uint32_t encode_word(uint32_t scale, float inv, Get g
     if (NOISE) {
         uint32_t t[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t[i] = noise_code(x[i], flipped(i), at(i));
-        w = pack_noise(t, x);
+        for (int i = 0; i < 8; ++i) t[i] = noise_code(x[i], noise(i), at(i));
+        w = pack_noise(t, signs());
     } else {
         w = encode8(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]);
     }
@@ -229,7 +256,7 @@ __device__ __forceinline__ void tile_rows_out(const uint8_t* tile, const uint8_t
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 const uint4 v = *reinterpret_cast<const uint4*>(noise + noise_chunk<TC>(r, blk * 2 + c));
-                nz[4 * c] = ~v.x; nz[4 * c + 1] = ~v.y; nz[4 * c + 2] = ~v.z; nz[4 * c + 3] = ~v.w;
+                nz[4 * c] = v.x; nz[4 * c + 1] = v.y; nz[4 * c + 2] = v.z; nz[4 * c + 3] = v.w;
             }
         }
 #pragma unroll
@@ -242,7 +269,7 @@ __device__ __forceinline__ void tile_rows_out(const uint8_t* tile, const uint8_t
         for (int k = 0; k < 4; ++k)
             codes[k] = encode_word<NOISE>(
                 s, inv, [&](int i) { return S::element(w, 8 * k + i); }, [&](int i) { return nz[2 * k + i / 4]; },
-                [](int i) { return i & 3; });
+                [](int i) { return i & 3; }, [&] { return S::signs(w + 8 * k / (4 / S::kBytes)); });
         bytes |= s << (8 * b);
         if (r < o.rows)
             *reinterpret_cast<uint4*>(o.codes + r * o.pitch + blk * 16) = make_uint4(codes[0], codes[1], codes[2], codes[3]);
@@ -283,14 +310,14 @@ __device__ __forceinline__ void tile_cols_out(const uint8_t* tile, const uint8_t
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const uint8_t* np = noise + noise_chunk<TC>(rb * 32 + 8 * k + i, c0 / 16) + c0 % 16;
-                    nz[i] = ~(W == 2 ? static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(np)) : static_cast<uint32_t>(*np));
+                    nz[i] = W == 2 ? static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(np)) : static_cast<uint32_t>(*np);
                 }
             }
 #pragma unroll
             for (int j = 0; j < W; ++j)
                 codes[j][k] = encode_word<NOISE>(
                     s[j], inv[j], [&](int i) { return W == 2 ? S::half(w[8 * k + i], j) : __uint_as_float(w[8 * k + i]); },
-                    [&](int i) { return nz[i]; }, [&](int) { return j; });
+                    [&](int i) { return nz[i]; }, [&](int) { return j; }, [&] { return S::signs_down(w + 8 * k, j); });
         }
 #pragma unroll
         for (int j = 0; j < W; ++j) {

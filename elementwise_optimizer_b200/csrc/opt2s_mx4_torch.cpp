@@ -325,8 +325,8 @@ struct Linear : torch::autograd::Function<Linear> {
     static torch::autograd::variable_list backward(Ctx* ctx, torch::autograd::variable_list grads)
     {
         const Tensor& dy = grads[0];
-        TORCH_CHECK_NOT_IMPLEMENTED(!(at::GradMode::is_enabled() && dy.requires_grad()),
-                                    "a 4-bit layer's gradient has no gradient of its own");
+        TORCH_CHECK_NOT_IMPLEMENTED(!at::GradMode::is_enabled(),
+                                    "a 4-bit layer's gradient has no gradient of its own (create_graph)");
         at::NoGradGuard no_grad;
         const auto saved = ctx->get_saved_variables();
         const auto facts = ctx->saved_data["facts"].toIntVector();

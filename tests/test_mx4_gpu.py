@@ -506,6 +506,14 @@ def test_refusals(mx4):
         torch.autograd.grad(y, xg, torch.ones_like(y).requires_grad_(), create_graph=True)
 
 
+def test_no_gradient_of_a_gradient_is_lost(mx4):
+    """dx depends on the weight whether or not dy asks for a gradient."""
+    x, w = (mixed(s, torch.float32, 221).requires_grad_() for s in ((4, 64), (8, 64)))
+    y = mx4.linear(x, w)
+    with pytest.raises(NotImplementedError):
+        torch.autograd.grad(y, x, torch.ones_like(y), create_graph=True)
+
+
 def test_as_many_groups_as_there_may_be(mx4):
     r = np.random.RandomState(3)
     counts = r.multinomial(700, np.full(1024, 1 / 1024)).tolist()
