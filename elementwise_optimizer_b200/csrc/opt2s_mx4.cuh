@@ -172,8 +172,27 @@ template <> struct Src<kF16> : Halves {
     __device__ static uint32_t magnitude(uint32_t bits) { return abs_bits(half(bits, 0)); }
 };
 
-// The largest magnitude of words of a 16-bit type, each half on its own.
-__device__ __forceinline__ uint32_t amax_halves(uint32_t amax, uint32_t w) { return __vmaxu2(amax, w & 0x7FFF7FFFu); }
+// The largest magnitudes of words of a 16-bit type, each half on its own: as
+// signed numbers the positive ones win, as unsigned ones the negative.
+struct Amax {
+    uint32_t pos = 0, any = 0;
+    __device__ void add(uint32_t v, uint32_t w)
+    {
+        pos = __vimax3_s16x2(pos, v, w);
+        any = __vimax3_u16x2(any, v, w);
+    }
+    __device__ uint32_t halves() const { return __vmaxu2(pos, any & 0x7FFF7FFFu); }
+};
+
+// Two bf16 elements times powers of two, in one instruction.  Exact but for
+// results below 2^-126, which round to the code 0 in every mode.
+__device__ __forceinline__ uint32_t scale_halves(uint32_t w, float lo, float hi)
+{
+    const uint32_t k = __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+    const __nv_bfloat162 x = __hmul2_rn(*reinterpret_cast<const __nv_bfloat162*>(&w),
+                                        *reinterpret_cast<const __nv_bfloat162*>(&k));
+    return *reinterpret_cast<const uint32_t*>(&x);
+}
 
 // One word of a block's codes: eight elements x times 2^-e.  noise(i) and
 // at(i) give element i's random byte as noise_code takes it, signs() theirs.
@@ -247,6 +266,7 @@ __device__ __forceinline__ void tile_rows_out(const uint8_t* tile, const uint8_t
     for (int b = 0; b < B; ++b) {
         const int blk = part * B + b;
         uint32_t w[4 * C], nz[8] = {}, amax = 0;
+        Amax most;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const uint4 v = *reinterpret_cast<const uint4*>(tile + tile_chunk<DT, TC>(r, blk * C + c));
@@ -260,15 +280,22 @@ __device__ __forceinline__ void tile_rows_out(const uint8_t* tile, const uint8_t
             }
         }
 #pragma unroll
-        for (int i = 0; i < 4 * C; ++i) amax = S::kBytes == 2 ? amax_halves(amax, w[i]) : max(amax, w[i] & 0x7FFFFFFFu);
-        if (S::kBytes == 2) amax = S::magnitude(max(amax & 0xFFFFu, amax >> 16));
+        for (int i = 0; i < 4 * C; i += 2) {
+            if (S::kBytes == 2) most.add(w[i], w[i + 1]);
+            else amax = max(amax, max(w[i] & 0x7FFFFFFFu, w[i + 1] & 0x7FFFFFFFu));
+        }
+        if (S::kBytes == 2) amax = S::magnitude(max(most.halves() & 0xFFFFu, most.halves() >> 16));
         const uint32_t s = scale_byte(amax);
         const float inv = inverse_scale(s);
+        if (DT == kBF16) {
+#pragma unroll
+            for (int i = 0; i < 4 * C; ++i) w[i] = scale_halves(w[i], inv, inv);
+        }
         uint32_t codes[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             codes[k] = encode_word<NOISE>(
-                s, inv, [&](int i) { return S::element(w, 8 * k + i); }, [&](int i) { return nz[2 * k + i / 4]; },
+                s, DT == kBF16 ? 1.0f : inv, [&](int i) { return S::element(w, 8 * k + i); }, [&](int i) { return nz[2 * k + i / 4]; },
                 [](int i) { return i & 3; }, [&] { return S::signs(w + 8 * k / (4 / S::kBytes)); });
         bytes |= s << (8 * b);
         if (r < o.rows)
@@ -291,17 +318,24 @@ __device__ __forceinline__ void tile_cols_out(const uint8_t* tile, const uint8_t
         const int c0 = (t % kAcross) * W, rb = t / kAcross;
         if (c0 >= o.scale_cols) continue;
         uint32_t w[32], amax = 0;
+        Amax most;
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
             w[i] = *reinterpret_cast<const uint32_t*>(tile + tile_chunk<DT, TC>(rb * 32 + i, c0 / P) + (c0 % P) * S::kBytes);
-            amax = W == 2 ? amax_halves(amax, w[i]) : max(amax, w[i] & 0x7FFFFFFFu);
+            if (W == 1) amax = max(amax, w[i] & 0x7FFFFFFFu);
+            else if (i & 1) most.add(w[i - 1], w[i]);
         }
+        if (W == 2) amax = most.halves();
         uint32_t s[W], codes[W][4];
         float inv[W];
 #pragma unroll
         for (int j = 0; j < W; ++j) {
             s[j] = scale_byte(W == 2 ? S::magnitude(j ? amax >> 16 : amax & 0xFFFFu) : amax);
             inv[j] = inverse_scale(s[j]);
+        }
+        if (DT == kBF16) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) w[i] = scale_halves(w[i], inv[0], inv[W - 1]);
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -316,7 +350,7 @@ __device__ __forceinline__ void tile_cols_out(const uint8_t* tile, const uint8_t
 #pragma unroll
             for (int j = 0; j < W; ++j)
                 codes[j][k] = encode_word<NOISE>(
-                    s[j], inv[j], [&](int i) { return W == 2 ? S::half(w[8 * k + i], j) : __uint_as_float(w[8 * k + i]); },
+                    s[j], DT == kBF16 ? 1.0f : inv[j], [&](int i) { return W == 2 ? S::half(w[8 * k + i], j) : __uint_as_float(w[8 * k + i]); },
                     [&](int i) { return nz[i]; }, [&](int) { return j; }, [&] { return S::signs_down(w + 8 * k, j); });
         }
 #pragma unroll
