@@ -184,16 +184,6 @@ struct Amax {
     __device__ uint32_t halves() const { return __vmaxu2(pos, any & 0x7FFF7FFFu); }
 };
 
-// Two bf16 elements times powers of two, in one instruction.  Exact but for
-// results below 2^-126, which round to the code 0 in every mode.
-__device__ __forceinline__ uint32_t scale_halves(uint32_t w, float lo, float hi)
-{
-    const uint32_t k = __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
-    const __nv_bfloat162 x = __hmul2_rn(*reinterpret_cast<const __nv_bfloat162*>(&w),
-                                        *reinterpret_cast<const __nv_bfloat162*>(&k));
-    return *reinterpret_cast<const uint32_t*>(&x);
-}
-
 // One word of a block's codes: eight elements x times 2^-e.  noise(i) and
 // at(i) give element i's random byte as noise_code takes it, signs() theirs.
 template <bool NOISE, typename Get, typename Noise, typename At, typename SignsOf>
@@ -287,15 +277,11 @@ __device__ __forceinline__ void tile_rows_out(const uint8_t* tile, const uint8_t
         if (S::kBytes == 2) amax = S::magnitude(max(most.halves() & 0xFFFFu, most.halves() >> 16));
         const uint32_t s = scale_byte(amax);
         const float inv = inverse_scale(s);
-        if (DT == kBF16) {
-#pragma unroll
-            for (int i = 0; i < 4 * C; ++i) w[i] = scale_halves(w[i], inv, inv);
-        }
         uint32_t codes[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             codes[k] = encode_word<NOISE>(
-                s, DT == kBF16 ? 1.0f : inv, [&](int i) { return S::element(w, 8 * k + i); }, [&](int i) { return nz[2 * k + i / 4]; },
+                s, inv, [&](int i) { return S::element(w, 8 * k + i); }, [&](int i) { return nz[2 * k + i / 4]; },
                 [](int i) { return i & 3; }, [&] { return S::signs(w + 8 * k / (4 / S::kBytes)); });
         bytes |= s << (8 * b);
         if (r < o.rows)
@@ -333,10 +319,6 @@ __device__ __forceinline__ void tile_cols_out(const uint8_t* tile, const uint8_t
             s[j] = scale_byte(W == 2 ? S::magnitude(j ? amax >> 16 : amax & 0xFFFFu) : amax);
             inv[j] = inverse_scale(s[j]);
         }
-        if (DT == kBF16) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) w[i] = scale_halves(w[i], inv[0], inv[W - 1]);
-        }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             uint32_t nz[8] = {};
@@ -350,7 +332,7 @@ __device__ __forceinline__ void tile_cols_out(const uint8_t* tile, const uint8_t
 #pragma unroll
             for (int j = 0; j < W; ++j)
                 codes[j][k] = encode_word<NOISE>(
-                    s[j], DT == kBF16 ? 1.0f : inv[j], [&](int i) { return W == 2 ? S::half(w[8 * k + i], j) : __uint_as_float(w[8 * k + i]); },
+                    s[j], inv[j], [&](int i) { return W == 2 ? S::half(w[8 * k + i], j) : __uint_as_float(w[8 * k + i]); },
                     [&](int i) { return nz[i]; }, [&](int) { return j; }, [&] { return S::signs_down(w + 8 * k, j); });
         }
 #pragma unroll

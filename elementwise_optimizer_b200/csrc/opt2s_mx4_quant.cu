@@ -4,13 +4,13 @@
 // (the contraction of the forward product) and in blocks down its columns,
 // transposed (the contraction of the backward products).  One CTA reads a
 // 128 x 128 tile once into shared memory and writes both forms from there.
-// A 4,096 x 8,192 bf16 source takes 24 us (4.2 TB/s of its 103 MB; 16 us at
-// the measured copy rate) and 43 us with noise (3.2 TB/s of 136 MB; 21 us):
-// instructions bound it, 15 an element and 34 with noise (62 % of the issue
-// slots, the ALU pipe 80 % busy with noise); fp32 reaches 5.8 TB/s.  Loads by
+// A 4,096 x 8,192 bf16 source takes 24 us (4.3 TB/s of its 103 MB; 16 us at
+// the measured copy rate) and 41 us with noise (3.3 TB/s of 136 MB; 21 us):
+// instructions bound it, 15 an element and 30 with noise (64 % of the issue
+// slots, the ALU pipe 77 % busy with noise); fp32 reaches 5.8 TB/s.  Loads by
 // cp.async, all of a tile's in flight at once; a persistent form that loaded
-// the next tile meanwhile was slower (27 and 55 us), and other numbers of
-// resident CTAs were no faster.
+// the next tile meanwhile was slower (27 and 55 us), other numbers of resident
+// CTAs were no faster, nor was scaling two bf16 elements at once.
 #include <type_traits>
 
 #include "opt2s_mx4.cuh"
