@@ -23,10 +23,42 @@ constexpr int kTileCols = 128;
 
 // A 16-byte copy from global to shared memory that does not wait; zeros when
 // !in (the address must then still be valid).
+__device__ __forceinline__ void copy16(uint8_t* dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                 :: "r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))), "l"(src) : "memory");
+}
 __device__ __forceinline__ void copy16(uint8_t* dst, const void* src, bool in)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
                  :: "r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+
+// The 16-byte chunks of a tile, CHUNKS a row of 16 * CHUNKS bytes from `x` on,
+// into shared memory (chunk c of row r at chunk c ^ (r & 7)); zeros from row
+// `rows` and chunk `chunks` on (`valid` is an address that may be read).  A
+// whole tile needs two instructions a chunk; with the bounds of a partial one
+// they were an eighth of all instructions.
+template <int CHUNKS>
+__device__ __forceinline__ void load_chunks(const uint8_t* x, int64_t pitch, int rows, int chunks, const void* valid,
+                                            uint8_t* dst, int tid)
+{
+    constexpr int kStep = kQuantThreads / CHUNKS;
+    static_assert(kStep % 8 == 0, "a thread's rows have one swizzle");
+    const int r0 = tid / CHUNKS, c = tid % CHUNKS;
+    const uint8_t* p = x + r0 * pitch + c * 16;
+    const int64_t step = pitch * kStep;
+    uint8_t* d = dst + r0 * CHUNKS * 16 + ((c ^ (r0 & 7)) << 4);
+    if (rows == kTileRows && chunks == CHUNKS) {
+#pragma unroll
+        for (int k = 0; k < kTileRows / kStep; ++k, p += step) copy16(d + k * kStep * CHUNKS * 16, p);
+    } else {
+#pragma unroll
+        for (int k = 0; k < kTileRows / kStep; ++k, p += step) {
+            const bool in = r0 + k * kStep < rows && c < chunks;
+            copy16(d + k * kStep * CHUNKS * 16, in ? p : valid, in);
+        }
+    }
 }
 
 // A tile of elements of B bytes whose rows do not start on 16 bytes: a warp
@@ -62,34 +94,20 @@ __device__ __forceinline__ void load_tile(const Mx4QuantArgs& a, int64_t row0, i
                                           uint8_t* tile, uint8_t* noise, int tid)
 {
     using S = Src<DT>;
-    constexpr int P = S::kPer, kChunks = kTileCols / P, kStep = kQuantThreads / kChunks;
+    constexpr int P = S::kPer;
     const int cols = static_cast<int>(min(static_cast<int64_t>(kTileCols), a.cols - col0));
-    {
-        const int c = tid % kChunks, at = c * P;
-        const uint8_t* x = static_cast<const uint8_t*>(a.x) + (slab * a.slab_stride + row0 * a.row_stride + col0) * S::kBytes;
-        if (a.vec && cols % P == 0) {
-            const int64_t pitch = a.row_stride * S::kBytes;
-            const uint8_t* p = x + c * 16;
-#pragma unroll
-            for (int r = tid / kChunks; r < kTileRows; r += kStep) {
-                const bool in = r < rows && at < cols;
-                copy16(tile + tile_chunk<DT, kTileCols>(r, c), in ? p + r * pitch : static_cast<const uint8_t*>(a.x), in);
-            }
-        } else {
-            load_elements<S::kBytes, kTileCols>(x, a.row_stride, rows, cols, tid, [&](int r, int e) {
-                return tile + tile_chunk<DT, kTileCols>(r, e / P) + e % P * S::kBytes;
-            });
-        }
+    const uint8_t* x = static_cast<const uint8_t*>(a.x) + (slab * a.slab_stride + row0 * a.row_stride + col0) * S::kBytes;
+    if (a.vec && cols % P == 0) {
+        load_chunks<kTileCols / P>(x, a.row_stride * S::kBytes, rows, cols / P, a.x, tile, tid);
+    } else {
+        load_elements<S::kBytes, kTileCols>(x, a.row_stride, rows, cols, tid, [&](int r, int e) {
+            return tile + tile_chunk<DT, kTileCols>(r, e / P) + e % P * S::kBytes;
+        });
     }
     if (NOISE) {
-        const int c = tid % 8, at = c * 16;
         const uint8_t* n = a.noise + (slab * a.rows + row0) * a.cols + col0;
         if (a.noise_vec && cols % 16 == 0) {
-#pragma unroll
-            for (int r = tid / 8; r < kTileRows; r += kQuantThreads / 8) {
-                const bool in = r < rows && at < cols;
-                copy16(noise + noise_chunk<kTileCols>(r, c), in ? n + r * a.cols + at : a.noise, in);
-            }
+            load_chunks<kTileCols / 16>(n, a.cols, rows, cols / 16, a.noise, noise, tid);
         } else {
             load_elements<1, kTileCols>(n, a.cols, rows, cols, tid,
                                         [&](int r, int e) { return noise + noise_chunk<kTileCols>(r, e / 16) + e % 16; });
