@@ -3,14 +3,15 @@
 // A quantised training step needs a matrix twice: in blocks along its rows
 // (the contraction of the forward product) and in blocks down its columns,
 // transposed (the contraction of the backward products).  One CTA reads a
-// 128 x 128 tile once into shared memory and writes both forms from there.
-// A 4,096 x 8,192 bf16 source takes 24 us (4.3 TB/s of its 103 MB; 16 us at
-// the measured copy rate) and 41 us with noise (3.3 TB/s of 136 MB; 21 us):
-// instructions bound it, 15 an element and 30 with noise (64 % of the issue
-// slots, the ALU pipe 77 % busy with noise); fp32 reaches 5.8 TB/s.  Loads by
-// cp.async, all of a tile's in flight at once; a persistent form that loaded
-// the next tile meanwhile was slower (27 and 55 us), other numbers of resident
-// CTAs were no faster, nor was scaling two bf16 elements at once.
+// 128 x 64 tile once into shared memory and writes both forms from there.
+// A 4,096 x 8,192 bf16 source takes 22 us (4.7 TB/s of its 103 MB; 16 us at
+// the measured copy rate) and 37 us with noise (3.7 TB/s of 136 MB; 21 us):
+// instructions bound it, 13 an element and 28 with noise, 15 of them on the
+// ALU pipe; fp32 reaches 6.1 TB/s.  Loads by cp.async, all of a tile's in
+// flight at once.  Tiles of 128 x 128 by 256 threads were slower (23 and 41 us:
+// fewer, larger steps between barriers and a coarser last wave), as was a
+// persistent form that loaded the next tile meanwhile (27 and 55 us); scaling
+// two bf16 elements at once changed nothing.
 #include <type_traits>
 
 #include "opt2s_mx4.cuh"
@@ -18,8 +19,8 @@
 namespace opt2s {
 namespace {
 
-constexpr int kQuantThreads = 256;
-constexpr int kTileCols = 128;
+constexpr int kQuantThreads = 128;
+constexpr int kTileCols = 64;
 
 // A 16-byte copy from global to shared memory that does not wait; zeros when
 // !in (the address must then still be valid).
@@ -44,11 +45,12 @@ __device__ __forceinline__ void load_chunks(const uint8_t* x, int64_t pitch, int
                                             uint8_t* dst, int tid)
 {
     constexpr int kStep = kQuantThreads / CHUNKS;
+    constexpr int kMask = CHUNKS < 8 ? CHUNKS - 1 : 7;
     static_assert(kStep % 8 == 0, "a thread's rows have one swizzle");
     const int r0 = tid / CHUNKS, c = tid % CHUNKS;
     const uint8_t* p = x + r0 * pitch + c * 16;
     const int64_t step = pitch * kStep;
-    uint8_t* d = dst + r0 * CHUNKS * 16 + ((c ^ (r0 & 7)) << 4);
+    uint8_t* d = dst + r0 * CHUNKS * 16 + ((c ^ (r0 & kMask)) << 4);
     if (rows == kTileRows && chunks == CHUNKS) {
 #pragma unroll
         for (int k = 0; k < kTileRows / kStep; ++k, p += step) copy16(d + k * kStep * CHUNKS * 16, p);
@@ -62,13 +64,13 @@ __device__ __forceinline__ void load_chunks(const uint8_t* x, int64_t pitch, int
 }
 
 // A tile of elements of B bytes whose rows do not start on 16 bytes: a warp
-// takes neighbouring elements of a row, four rows in flight.  `place` says
+// takes neighbouring elements of a row, eight rows in flight.  `place` says
 // where an element goes.
 template <int B, int COLS, typename Place>
 __device__ __forceinline__ void load_elements(const uint8_t* x, int64_t pitch, int rows, int cols, int tid, Place place)
 {
     using T = std::conditional_t<B == 4, uint32_t, std::conditional_t<B == 2, uint16_t, uint8_t>>;
-    constexpr int kAcross = COLS / 32, kRows = 4;
+    constexpr int kAcross = COLS / 32, kRows = 8;
     const T* p = reinterpret_cast<const T*>(x);
     const int lane = tid & 31;
     for (int r0 = (tid >> 5) * kRows; r0 < kTileRows; r0 += kQuantThreads / 32 * kRows) {
@@ -146,13 +148,12 @@ __global__ void __launch_bounds__(kQuantThreads) mx4_quantize_kernel(const Mx4Qu
     copies_done();
     __syncthreads();
     TileOut o{};
-    const int64_t cg = col0 / 128;                  // 128-column group of the row form
     if (a.codes && rows > 0) {
         // the last tile of an ungrouped matrix also writes the scale bytes of its padding rows
         const int64_t rp = (a.rows + 3) / 4 * 4;
         o.pitch = (a.cols + 127) / 128 * 64;
-        o.codes = a.codes + (slab * a.rows + row0) * o.pitch + cg * 64;
-        o.scales = a.scales + ((cg * a.slabs + slab) * rp + row0) * 4;
+        o.codes = a.codes + (slab * a.rows + row0) * o.pitch + col0 / 2;
+        o.scales = a.scales + ((col0 / 128 * a.slabs + slab) * rp + row0) * 4 + col0 % 128 / 32;
         o.rows = rows;
         o.scale_rows = row_end == a.rows ? static_cast<int>(min(static_cast<int64_t>(kTileRows), rp - row0)) : rows;
         tile_rows_out<DT, kTileCols, NOISE, kQuantThreads>(tile, noise, o, tid);
@@ -283,7 +284,7 @@ cudaError_t launch_quantize_dt(const Mx4QuantArgs& a, dim3 grid, cudaStream_t st
 
 cudaError_t launch_mx4_quantize(const Mx4QuantArgs& a, int dtype, int64_t row_tiles, cudaStream_t stream)
 {
-    const dim3 grid(static_cast<unsigned>((a.cols + kTileCols - 1) / kTileCols), static_cast<unsigned>(row_tiles),
+    const dim3 grid(static_cast<unsigned>((a.cols + 127) / 128 * (128 / kTileCols)), static_cast<unsigned>(row_tiles),
                     static_cast<unsigned>(a.slabs));
     if (dtype == kF32) return launch_quantize_dt<kF32>(a, grid, stream);
     if (dtype == kF16) return launch_quantize_dt<kF16>(a, grid, stream);
