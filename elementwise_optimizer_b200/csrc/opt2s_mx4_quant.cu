@@ -6,8 +6,8 @@
 // 128 x 64 tile once into shared memory and writes both forms from there.
 // A 4,096 x 8,192 bf16 source takes 22 us (4.7 TB/s of its 103 MB; 16 us at
 // the measured copy rate) and 37 us with noise (3.7 TB/s of 136 MB; 21 us):
-// instructions bound it, 13 an element and 28 with noise, 15 of them on the
-// ALU pipe; fp32 reaches 6.1 TB/s.  Loads by cp.async, all of a tile's in
+// instructions bound it, 13 an element and 27 with noise (the ALU pipe 76 %
+// busy); fp32 reaches 6.1 TB/s.  Loads by cp.async, all of a tile's in
 // flight at once.  Tiles of 128 x 128 by 256 threads were slower (23 and 41 us:
 // fewer, larger steps between barriers and a coarser last wave), as was a
 // persistent form that loaded the next tile meanwhile (27 and 55 us); scaling
