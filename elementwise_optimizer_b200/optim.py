@@ -300,8 +300,15 @@ class TwoStateOptimizer(torch.optim.Optimizer):
     def mx4_copies(self, p):
         """The pair of 4-bit forms of parameter p that the steps keep up to
         date (made from p at the first call)."""
-        if not self._has_mx4(p):
-            raise ValueError("this parameter has no 4-bit copies (see the mx4 argument)")
+        if p not in self._mx4_pairs:
+            # a tensor that no step writes would keep the copies of its value at the first call
+            if not any(q is p for g in self.param_groups for q in g["params"]):
+                raise ValueError("not a parameter of this optimizer, so its steps keep no copies of it")
+            if not self._has_mx4(p):
+                raise ValueError("this parameter has no 4-bit copies (see the mx4 argument)")
+        return self._mx4_pair(p)
+
+    def _mx4_pair(self, p):
         pair = self._mx4_pairs.get(p)
         if pair is None:
             from . import mx4
@@ -397,7 +404,7 @@ class TwoStateOptimizer(torch.optim.Optimizer):
         if self._mx4 is not False:
             return B.TensorListMX4.from_tensors(
                 ps, [p.grad for p in ps], [s["state1"] for s in states], [s["state2"] for s in states],
-                [self.mx4_copies(p) if self._has_mx4(p) else None for p in ps])
+                [self._mx4_pair(p) if self._has_mx4(p) else None for p in ps])
         return B.TensorList.from_tensors(ps, [p.grad for p in ps], [s["state1"] for s in states],
                                          [s["state2"] for s in states])
 

@@ -1,0 +1,44 @@
+"""How the 4-bit operators are used: kept copies, outputs that are changed in
+place, sums into given tensors, and the report of waits that gave up."""
+import ctypes
+
+import pytest
+import torch
+
+from tests.mx4_support import close, product_bound, round_ref, turned_ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture
+def mx4():
+    from elementwise_optimizer_b200 import binding, mx4 as m
+    yield m
+    n = ctypes.c_uint32()
+    binding.check(binding.lib().opt2s_mx4_errors(ctypes.byref(n)), "opt2s_mx4_errors")
+    assert n.value == 0
+
+
+def normal(shape, seed, scale=1.0, dtype=torch.float32):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * scale).to(dtype).cuda()
+
+
+def offsets_of(counts):
+    return torch.tensor([0] + counts, dtype=torch.int32).cumsum(0, dtype=torch.int32).cuda()
+
+
+def test_copies_of_a_group_added_later(mx4):
+    from elementwise_optimizer_b200 import optim
+    a, b, foreign = (torch.nn.Parameter(normal((40, 96), s)) for s in (1, 2, 3))
+    opt = optim.AdamW32bit([a], lr=1e-2, mx4=True)
+    for p in (b, foreign):
+        with pytest.raises(ValueError, match="not a parameter of this optimizer"):
+            opt.mx4_copies(p)
+    opt.add_param_group({"params": [b]})
+    pair = opt.mx4_copies(b)
+    a.grad, b.grad = torch.ones_like(a), torch.ones_like(b)
+    opt.step()
+    assert opt.mx4_copies(b) is pair
+    for got, want in zip(pair, mx4.quantize_pair(b)):
+        assert torch.equal(got.codes, want.codes) and torch.equal(got.scales, want.scales)
