@@ -507,9 +507,11 @@ def opt2s_step_8bit(tl: "TensorList8", hyper: Hyper, step: int, stream=None) -> 
 
 def opt2s_step_mx4(tl: "TensorListMX4", hyper: Hyper, step: int, stream=None) -> None:
     """opt2s_step that also writes the 4-bit copies of the updated params (one
-    launch for up to 256 tensors)."""
+    launch for up to 256 tensors).  A graph that saved the copies before the
+    step refuses to use them after it."""
     check(lib().opt2s_step_mx4(ctypes.byref(tl.desc), ctypes.byref(hyper), int(step),
                                _stream_handle(stream)), "opt2s_step_mx4")
+    bump_versions(tl.written)
 
 
 def state_bits_for(numel: int, min_8bit_size: int = MIN_8BIT_SIZE) -> int:

@@ -455,7 +455,6 @@ class TwoStateOptimizer(torch.optim.Optimizer):
         """One step of a group's records (not capturable)."""
         if self._mx4 is not False:
             B.opt2s_step_mx4(tl, hyper, step)
-            B.bump_versions(tl.written)      # a graph that saved the copies before this step must not use them
         elif self.lamb:
             B.opt2s_step_lamb(tl, hyper, step)
         elif self.max_unorm > 0.0:

@@ -42,3 +42,19 @@ def test_copies_of_a_group_added_later(mx4):
     assert opt.mx4_copies(b) is pair
     for got, want in zip(pair, mx4.quantize_pair(b)):
         assert torch.equal(got.codes, want.codes) and torch.equal(got.scales, want.scales)
+
+
+def test_a_step_between_forward_and_backward_is_noticed(mx4):
+    """opt2s_step_mx4 writes the copies in place: a graph that saved them
+    before must not use them, as after quantize_pair(out=)."""
+    from elementwise_optimizer_b200 import binding as B
+    w, grad, m, v = normal((40, 96), 11), normal((40, 96), 12), *(torch.zeros(40 * 96, device="cuda") for _ in range(2))
+    pair = mx4.quantize_pair(w)
+    tl = B.TensorListMX4.from_tensors([w], [grad], [m], [v], [pair])
+    x = normal((9, 96), 13).requires_grad_()
+    y = mx4.linear(x, w, copies=pair)
+    mx4.opt2s_step_mx4(tl, B.make_hyper("adam", lr=0.1), 1)
+    with pytest.raises(RuntimeError, match="inplace"):
+        y.sum().backward()
+    mx4.linear(x, w, copies=pair).sum().backward()
+    assert torch.equal(x.grad, torch.autograd.grad(mx4.linear(x, w).sum(), x)[0])

@@ -16,3 +16,37 @@ def test_copies_only_of_the_optimizers_own_parameters():
         with pytest.raises(ValueError, match="not a parameter of this optimizer"):
             opt.mx4_copies(own.detach())
         assert not opt._mx4_pairs
+
+
+def test_the_step_tells_autograd_that_it_wrote_the_copies(monkeypatch):
+    """Called by itself as by an optimizer; a step that fails writes nothing."""
+    from types import SimpleNamespace
+
+    from elementwise_optimizer_b200 import binding as B
+    p, g, m, v = torch.zeros(4, 8), torch.zeros(4, 8), torch.zeros(32), torch.zeros(32)
+
+    def form(rows, cols):
+        return SimpleNamespace(slabs=1, rows=rows, cols=cols, shape=(rows, cols), device=p.device,
+                               codes=torch.zeros(rows, 64, dtype=torch.uint8), scales=torch.zeros(16, dtype=torch.uint8))
+
+    pair = (form(4, 8), form(8, 4))
+    tl = B.TensorListMX4.from_tensors([p], [g], [m], [v], [pair])
+    library = B.lib()
+    status = 0
+
+    class Fake:
+        opt2s_error_string, opt2s_last_cuda_error = library.opt2s_error_string, library.opt2s_last_cuda_error
+
+        @staticmethod
+        def opt2s_step_mx4(*args):
+            return status
+
+    monkeypatch.setattr(B, "lib", lambda: Fake)
+    monkeypatch.setattr(B, "_stream_handle", lambda stream: None)
+    before = [f.codes._version for f in pair]
+    B.opt2s_step_mx4(tl, B.make_hyper("adam"), 1)
+    assert [f.codes._version for f in pair] == [n + 1 for n in before]
+    status = -1
+    with pytest.raises(B.Opt2sError):
+        B.opt2s_step_mx4(tl, B.make_hyper("adam"), 1)
+    assert [f.codes._version for f in pair] == [n + 1 for n in before]
