@@ -312,7 +312,8 @@ class TwoStateOptimizer(torch.optim.Optimizer):
         pair = self._mx4_pairs.get(p)
         if pair is None:
             from . import mx4
-            pair = self._mx4_pairs[p] = mx4.quantize_pair(p)
+            with torch.inference_mode(False):      # an evaluation may ask first, a graph must be able to save them later
+                pair = self._mx4_pairs[p] = mx4.quantize_pair(p)
         return pair
 
     def refresh_mx4(self) -> None:

@@ -58,3 +58,23 @@ def test_a_step_between_forward_and_backward_is_noticed(mx4):
         y.sum().backward()
     mx4.linear(x, w, copies=pair).sum().backward()
     assert torch.equal(x.grad, torch.autograd.grad(mx4.linear(x, w).sum(), x)[0])
+
+
+def test_copies_first_asked_for_in_inference_mode(mx4):
+    """An evaluation before the training: the copies that the optimizer keeps
+    can be saved by a graph afterwards."""
+    from elementwise_optimizer_b200 import optim
+    w = torch.nn.Parameter(normal((40, 96), 21))
+    opt = optim.AdamW32bit([w], lr=1e-2, mx4=True)
+    x = normal((9, 96), 22).requires_grad_()
+    with torch.inference_mode():
+        want = mx4.linear(x, w, copies=opt.mx4_copies(w))
+    for _ in range(2):
+        y = mx4.linear(x, w, copies=opt.mx4_copies(w))
+        assert torch.equal(y, mx4.linear(x, w)) and (want is None or torch.equal(y, want))
+        want = None
+        y.sum().backward()
+        opt.step()
+        opt.zero_grad()
+        with torch.inference_mode():
+            opt.refresh_mx4()

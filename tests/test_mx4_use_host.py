@@ -50,3 +50,15 @@ def test_the_step_tells_autograd_that_it_wrote_the_copies(monkeypatch):
     with pytest.raises(B.Opt2sError):
         B.opt2s_step_mx4(tl, B.make_hyper("adam"), 1)
     assert [f.codes._version for f in pair] == [n + 1 for n in before]
+
+
+def test_kept_copies_are_no_inference_tensors(monkeypatch):
+    """A graph may save them, wherever they were first asked for."""
+    from elementwise_optimizer_b200 import mx4
+    monkeypatch.setattr(mx4, "quantize_pair", lambda p: (torch.empty(1), torch.empty(1)))
+    own = torch.nn.Parameter(torch.zeros(4, 4))
+    opt = optim.AdamW32bit([own], mx4=True)
+    with torch.inference_mode():
+        pair = opt.mx4_copies(own)
+        assert torch.empty(1).is_inference()
+    assert not any(t.is_inference() for t in pair) and opt.mx4_copies(own) is pair
