@@ -299,7 +299,8 @@ class TwoStateOptimizer(torch.optim.Optimizer):
 
     def mx4_copies(self, p):
         """The pair of 4-bit forms of parameter p that the steps keep up to
-        date (made from p at the first call)."""
+        date (made from p at the first call, which may not be captured in a
+        CUDA graph)."""
         if p not in self._mx4_pairs:
             # a tensor that no step writes would keep the copies of its value at the first call
             if not any(q is p for g in self.param_groups for q in g["params"]):
@@ -312,6 +313,9 @@ class TwoStateOptimizer(torch.optim.Optimizer):
         pair = self._mx4_pairs.get(p)
         if pair is None:
             from . import mx4
+            if p.is_cuda and torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("a parameter's 4-bit copies are made at the first mx4_copies or step: call "
+                                   "it before the capture, which would only record their quantisation")
             with torch.inference_mode(False):      # an evaluation may ask first, a graph must be able to save them later
                 pair = self._mx4_pairs[p] = mx4.quantize_pair(p)
         return pair

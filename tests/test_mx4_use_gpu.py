@@ -78,3 +78,23 @@ def test_copies_first_asked_for_in_inference_mode(mx4):
         opt.zero_grad()
         with torch.inference_mode():
             opt.refresh_mx4()
+
+
+def test_copies_first_asked_for_under_capture(mx4):
+    """A captured quantisation has not run when the capture ends, so what the
+    optimizer would keep from then on holds no copies yet."""
+    from elementwise_optimizer_b200 import optim
+    w = torch.nn.Parameter(normal((40, 96), 23))
+    opt = optim.AdamW32bit([w], lr=1e-2, mx4=True)
+    x = normal((9, 96), 24)
+    want = mx4.linear(x, w).detach()
+    with torch.cuda.graph(torch.cuda.CUDAGraph()):
+        x + 1
+        with pytest.raises(RuntimeError, match="before the capture"):
+            opt.mx4_copies(w)
+    opt.mx4_copies(w)
+    graph = torch.cuda.CUDAGraph()
+    with torch.no_grad(), torch.cuda.graph(graph):
+        y = mx4.linear(x, w, copies=opt.mx4_copies(w))
+    graph.replay()
+    assert torch.equal(y, want) and torch.equal(mx4.linear(x, w, copies=opt.mx4_copies(w)), want)
