@@ -199,9 +199,12 @@ void quantize(const Tensor& x, const OptTensor& noise, const OptTensor& offsets,
     run_job(j, q ? &cq : nullptr, qt ? &ct : nullptr, x.device());
 }
 
-// The three products; d is [rows, cols] or [groups, rows, cols].
+// The three products; d is [rows, cols] or [groups, rows, cols], or has the
+// shape `as` of as many elements where it is made here.  (A view of a matrix
+// could not be changed in place: autograd refuses that for a view made inside
+// a function or without gradients.)
 Tensor product(const opt2s_mx4& a, const opt2s_mx4& b, const at::Device& device, const OptTensor& offsets, bool ragged,
-               c10::ScalarType dtype, const OptTensor& given, bool accumulate)
+               c10::ScalarType dtype, const OptTensor& given, bool accumulate, at::IntArrayRef as = {})
 {
     TORCH_CHECK_VALUE(a.cols == b.cols, message("the contractions differ: ", a.cols, " and ", b.cols));
     TORCH_CHECK_VALUE(a.slabs == 1, "the first operand of a product is a single matrix");
@@ -227,7 +230,7 @@ Tensor product(const opt2s_mx4& a, const opt2s_mx4& b, const at::Device& device,
         if (!d.is_inference()) d.unsafeGetTensorImpl()->bump_version();       // autograd sees the write
     } else {
         TORCH_CHECK_VALUE(!accumulate, "accumulate needs the tensor to add to (out)");
-        d = at::empty(shape, at::TensorOptions().dtype(dtype).device(device));
+        d = at::empty(as.empty() ? at::IntArrayRef(shape) : as, at::TensorOptions().dtype(dtype).device(device));
     }
     const int32_t code = dtype_code(d.scalar_type()), acc = accumulate ? 1 : 0;
     void* out = d.numel() ? d.data_ptr() : nullptr;
@@ -248,9 +251,18 @@ Tensor rows_of(const Tensor& x)
     return m.size(-1) <= 1 || m.stride(-1) == 1 ? m : m.contiguous();
 }
 
-Tensor times(const opt2s_mx4& a, const opt2s_mx4& b, const at::Device& device, const OptTensor& offsets, c10::ScalarType dtype)
+Tensor times(const opt2s_mx4& a, const opt2s_mx4& b, const at::Device& device, const OptTensor& offsets, c10::ScalarType dtype,
+             at::IntArrayRef as)
 {
-    return product(a, b, device, offsets, false, dtype, std::nullopt, false);
+    return product(a, b, device, offsets, false, dtype, std::nullopt, false, as);
+}
+
+// x's shape with n columns.
+std::vector<int64_t> with_columns(const Tensor& x, int64_t n)
+{
+    std::vector<int64_t> shape = x.sizes().vec();
+    shape.back() = n;
+    return shape;
 }
 
 Tensor project(const Tensor& x, const Matrix& w, const OptTensor& offsets, std::optional<c10::ScalarType> dtype)
@@ -265,24 +277,20 @@ Tensor project(const Tensor& x, const Matrix& w, const OptTensor& offsets, std::
     TORCH_CHECK_VALUE(w.slabs == slabs, message("the weight has ", w.slabs, " slabs where this product takes ", slabs));
     const c10::ScalarType out = dtype.value_or(x.scalar_type());
     const Tensor rows = rows_of(x);
-    Tensor y;
+    const std::vector<int64_t> shape = with_columns(x, w.rows);
     if (rows.size(0) == 1 && !offsets && w.cols <= OPT2S_MX4_PROJECT_COLS) {
         // one row: 1 x 8,192 x 2,048 takes 5.6 us in one launch and 8.4 us in two
         const c10::cuda::CUDAGuard guard(device);
-        y = at::empty({1, w.rows}, at::TensorOptions().dtype(out).device(device));
+        Tensor y = at::empty(shape, at::TensorOptions().dtype(out).device(device));
         const opt2s_mx4 cw = w.c();
         check(lib.project_row(rows.data_ptr(), w.cols, dtype_code(x.scalar_type()), &cw, y.numel() ? y.data_ptr() : nullptr,
                               dtype_code(out), stream_of(device)),
               "opt2s_mx4_project_row");
-    } else {
-        Packed q;
-        quantize(rows, std::nullopt, std::nullopt, &q, nullptr);
-        y = times(q.c, w.c(), device, offsets, out);
+        return y;
     }
-    if (x.dim() == 2) return y;
-    std::vector<int64_t> shape = x.sizes().vec();
-    shape.back() = w.rows;
-    return y.view(shape);
+    Packed q;
+    quantize(rows, std::nullopt, std::nullopt, &q, nullptr);
+    return times(q.c, w.c(), device, offsets, out, shape);
 }
 
 // y = Q(x) Q(w)^T with the straight-through gradients
@@ -315,11 +323,7 @@ struct Linear : torch::autograd::Function<Linear> {
             facts.insert(facts.end(), x.sizes().begin(), x.sizes().end());
             ctx->saved_data["facts"] = std::move(facts);
         }
-        Tensor y = times(xq.c, w, device, offsets, x.scalar_type());
-        if (x.dim() == 2) return y;
-        std::vector<int64_t> shape = x.sizes().vec();
-        shape.back() = w.rows;
-        return y.view(shape);
+        return times(xq.c, w, device, offsets, x.scalar_type(), with_columns(x, w.rows));
     }
 
     static torch::autograd::variable_list backward(Ctx* ctx, torch::autograd::variable_list grads)
@@ -349,8 +353,7 @@ struct Linear : torch::autograd::Function<Linear> {
             quantize(rows, noise, need_w ? offsets : std::nullopt, need_x ? &dq : nullptr, need_w ? &dt : nullptr);
             if (need_x) {
                 const opt2s_mx4 wt = saved[1].defined() ? Matrix{saved[0], saved[1], slabs, k, n}.c() : packed_view(saved[0], slabs, k, n);
-                dx = times(dq.c, wt, device, offsets, dy.scalar_type());
-                if (x_shape.size() != 2) dx = dx.view(x_shape);
+                dx = times(dq.c, wt, device, offsets, dy.scalar_type(), x_shape);
             }
             if (need_w)
                 dw = product(dt.c, packed_view(saved[2], 1, k, facts[3]), device, offsets, offsets.has_value(), w_dtype, std::nullopt, false);
@@ -379,8 +382,7 @@ Tensor linear(const Tensor& x, const Tensor& weight, const OptTensor& offsets, c
     }
     OptTensor bytes;
     if (noise) {
-        std::vector<int64_t> want = x.sizes().vec();
-        want.back() = n;
+        const std::vector<int64_t> want = with_columns(x, n);
         TORCH_CHECK_VALUE(noise->scalar_type() == at::kByte && noise->sizes() == at::IntArrayRef(want) &&
                               noise->device() == x.device(),
                           message("noise must be a uint8 tensor of the output's shape ", at::IntArrayRef(want), " on ", x.device()));

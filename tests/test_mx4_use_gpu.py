@@ -98,3 +98,27 @@ def test_copies_first_asked_for_under_capture(mx4):
         y = mx4.linear(x, w, copies=opt.mx4_copies(w))
     graph.replay()
     assert torch.equal(y, want) and torch.equal(mx4.linear(x, w, copies=opt.mx4_copies(w)), want)
+
+
+@pytest.mark.parametrize("shape", [(96,), (9, 96), (3, 4, 96), (0, 4, 96)])
+def test_outputs_may_be_changed_in_place(mx4, shape):
+    """A bias or a residual added in place, as to any layer's output."""
+    w, bias = (normal(s, 31).requires_grad_() for s in ((40, 96), (40,)))
+    x = normal(shape, 32).requires_grad_()
+    dy = normal((*shape[:-1], 40), 33)
+    y = mx4.linear(x, w)
+    plain = y + bias
+    want = torch.autograd.grad(plain, (x, w, bias), dy, retain_graph=True)
+    y += bias
+    assert torch.equal(y, plain)
+    for a, b in zip(torch.autograd.grad(y, (x, w, bias), dy), want):
+        assert torch.equal(a, b)
+    served = mx4.project(x, mx4.quantize(w))
+    plain = served + bias
+    served += bias
+    assert torch.equal(served, plain)
+    assert torch.equal(torch.autograd.grad(served, bias, dy)[0], want[2])
+    # the gradient too, as a leaf's
+    mx4.linear(x, w).backward(dy)
+    x.grad += bias.sum()
+    assert x.grad.requires_grad
