@@ -1096,6 +1096,11 @@ cudaError_t launch_mx4_gemm(Mx4GemmArgs a, const Mx4GemmOperands& op, cudaStream
                                                                : launch_as<128, false, false>(a, op, sms, stream);
 }
 
-cudaError_t mx4_error_count(unsigned int* out) { return cudaMemcpyFromSymbol(out, g_mx4_errors, sizeof(*out)); }
+cudaError_t mx4_error_count(unsigned int* out)
+{
+    // the copy's own stream does not wait for streams made non-blocking
+    const cudaError_t e = cudaDeviceSynchronize();
+    return e != cudaSuccess ? e : cudaMemcpyFromSymbol(out, g_mx4_errors, sizeof(*out));
+}
 
 }  // namespace opt2s

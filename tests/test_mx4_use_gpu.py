@@ -122,3 +122,17 @@ def test_outputs_may_be_changed_in_place(mx4, shape):
     mx4.linear(x, w).backward(dy)
     x.grad += bias.sum()
     assert x.grad.requires_grad
+
+
+def test_the_error_count_waits_for_every_stream():
+    """opt2s_mx4_errors speaks of all products in flight, those on streams
+    that the legacy stream does not wait for included."""
+    from elementwise_optimizer_b200 import binding
+    n = ctypes.c_uint32()
+    stream, done = torch.cuda.Stream(), torch.cuda.Event()
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(200_000_000)               # 0.1 s
+        done.record()
+    assert not done.query()
+    binding.check(binding.lib().opt2s_mx4_errors(ctypes.byref(n)), "opt2s_mx4_errors")
+    assert done.query() and n.value == 0
