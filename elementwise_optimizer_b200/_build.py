@@ -42,7 +42,7 @@ API = "opt2s_api.cpp"
 TESTING_ONLY = ["opt2s_testing.cu"]
 SOURCES = [os.path.join(CSRC, f) for f in COMMON + [API] + TESTING_ONLY]
 HEADERS = [os.path.join(CSRC, "opt2s_internal.h"), os.path.join(CSRC, "opt2s_device.cuh"),
-           os.path.join(CSRC, "opt2s_mx4.cuh"),
+           os.path.join(CSRC, "opt2s_mx4.cuh"), os.path.join(CSRC, "opt2s_mx4_wait.cuh"),
            os.path.join(INCLUDE, "opt2s.h"), os.path.join(INCLUDE, "opt2s_testing.h")]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

@@ -209,13 +209,16 @@ EXPORTS = {
                                                           ctypes.c_int64]),
     "opt2s_testing_check_division": (ctypes.c_int, [ctypes.c_uint64, ctypes.c_int64, ctypes.c_int32,
                                                     ctypes.POINTER(ctypes.c_int64)]),
+    "opt2s_testing_wait_runs_out": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int32, ctypes.c_uint32,
+                                                   ctypes.POINTER(ctypes.c_uint32)]),
     "opt2s_testing_max_block_threads": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int32]),
     "opt2s_testing_quant_tables": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32), ctypes.c_int64]),
 }
 
 # exported by the test build only
 TESTING_ONLY = {"opt2s_testing_set_chunk_elems", "opt2s_testing_set_launch",
-                "opt2s_testing_fail_allocs", "opt2s_testing_check_division"}
+                "opt2s_testing_fail_allocs", "opt2s_testing_check_division",
+                "opt2s_testing_wait_runs_out"}
 
 _libs = {}
 _use_testing = False
@@ -677,6 +680,13 @@ def testing_check_division(seed: int, n: int, mode: int) -> int:
     check(_testing_lib().opt2s_testing_check_division(seed, n, mode, ctypes.byref(out)),
           "check_division")
     return int(out.value)
+
+
+def testing_wait_runs_out(ctas: int, threads: int, limit: int) -> tuple:
+    """(what the CTAs added to the error count, threads that gave up)."""
+    out = (ctypes.c_uint32 * 2)()
+    check(_testing_lib().opt2s_testing_wait_runs_out(ctas, threads, limit, out), "wait_runs_out")
+    return tuple(out)
 
 
 def testing_choose_chunk_elems(tl: TensorList, resident_warps: int) -> int:

@@ -852,4 +852,17 @@ OPT2S_API int opt2s_testing_check_division(uint64_t seed, int64_t n, int32_t mod
     *mismatches = static_cast<int64_t>(h);
     return OPT2S_OK;
 }
+
+OPT2S_API int opt2s_testing_wait_runs_out(int32_t ctas, int32_t threads, uint32_t limit, uint32_t* counts)
+{
+    if (!counts || ctas < 1 || threads < 1 || threads > 1024 || limit > (1u << 16)) return OPT2S_ERR_INVALID_ARG;
+    unsigned int* d = nullptr;
+    cudaError_t e = cudaMalloc(&d, 2 * sizeof(*d));
+    if (e != cudaSuccess) return cuda_fail(e);
+    e = cudaMemset(d, 0, 2 * sizeof(*d));
+    if (e == cudaSuccess) e = opt2s::wait_runs_out(ctas, threads, limit, d, 0);
+    if (e == cudaSuccess) e = cudaMemcpy(counts, d, 2 * sizeof(*d), cudaMemcpyDeviceToHost);
+    cudaFree(d);
+    return e != cudaSuccess ? cuda_fail(e) : OPT2S_OK;
+}
 #endif  // OPT2S_TESTING

@@ -246,6 +246,8 @@ cudaError_t max_block_threads(int algo, int skip_zeros, int only, int* out);
 // from __fdiv_rn (mode 0: any x; mode 1: x/d near a rounding boundary).
 cudaError_t check_division(uint64_t seed, int64_t n, int mode, unsigned long long* d_count,
                            cudaStream_t stream);
+// Test build only: CTAs whose threads wait for what never comes (see opt2s_testing.h).
+cudaError_t wait_runs_out(int ctas, int threads, uint32_t limit, unsigned int* d_counts, cudaStream_t stream);
 
 // Number of blocks a launch of `nchunks` chunks uses on the current device.
 cudaError_t grid_for(int64_t nchunks, int algo, int skip_zeros, int only,

@@ -32,6 +32,7 @@
 #include <cuda.h>
 
 #include "opt2s_mx4.cuh"
+#include "opt2s_mx4_wait.cuh"
 
 namespace opt2s {
 namespace {
@@ -47,10 +48,6 @@ __device__ unsigned int g_mx4_errors;
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
-__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count)
-{
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" :: "r"(bar), "r"(count) : "memory");
-}
 __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes)
 {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" :: "r"(bar), "r"(bytes) : "memory");
@@ -58,14 +55,6 @@ __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes)
 __device__ __forceinline__ void bar_arrive(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
-}
-__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
-{
-    uint32_t done;
-    asm volatile("{\n\t.reg .pred p;\n\t"
-                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-                 "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(done) : "r"(bar), "r"(parity) : "memory");
-    return done != 0;
 }
 
 __device__ __forceinline__ uint32_t in_rank(uint32_t addr, int rank)      // addr in another CTA of the cluster
@@ -86,16 +75,9 @@ __device__ __forceinline__ bool elect_one()
     return p != 0;
 }
 
-// Bounded wait; false when it ran out or the CTA is aborting.
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag)
 {
-    for (uint32_t i = 0; i < kWaitLimit; ++i) {
-        if (bar_try(bar, parity)) return true;
-        if ((i & 255u) == 255u && *abort_flag) return false;
-    }
-    *abort_flag = 1;
-    atomicAdd(&g_mx4_errors, 1u);
-    return false;
+    return bar_wait(bar, parity, kWaitLimit, abort_flag, &g_mx4_errors);
 }
 
 // The same by a whole warp, which then goes on or stops as one.

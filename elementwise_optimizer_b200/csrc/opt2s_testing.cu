@@ -7,6 +7,7 @@
 // public API.
 
 #include "opt2s_device.cuh"
+#include "opt2s_mx4_wait.cuh"
 
 namespace opt2s {
 namespace {
@@ -88,12 +89,33 @@ __global__ void check_division_kernel(uint64_t seed, int64_t n, int mode,
     if (bad) atomicAdd(mismatches, bad);
 }
 
+// Every thread waits for a barrier that nothing completes, `limit` attempts
+// at most: what a product's CTA does when its copies do not come.
+__global__ void wait_runs_out_kernel(uint32_t limit, unsigned int* errors, unsigned int* returned)
+{
+    __shared__ __align__(8) uint64_t bar;
+    __shared__ volatile int abort_flag;
+    const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(&bar));
+    if (threadIdx.x == 0) {
+        bar_init(at, 1);
+        abort_flag = 0;
+    }
+    __syncthreads();
+    if (!bar_wait(at, 0, limit, &abort_flag, errors)) atomicAdd(returned, 1u);
+}
+
 }  // namespace
 
 cudaError_t check_division(uint64_t seed, int64_t n, int mode, unsigned long long* d_count,
                            cudaStream_t stream)
 {
     check_division_kernel<<<148 * 8, 256, 0, stream>>>(seed, n, mode, d_count);
+    return cudaGetLastError();
+}
+
+cudaError_t wait_runs_out(int ctas, int threads, uint32_t limit, unsigned int* d_counts, cudaStream_t stream)
+{
+    wait_runs_out_kernel<<<ctas, threads, 0, stream>>>(limit, d_counts, d_counts + 1);
     return cudaGetLastError();
 }
 

@@ -530,8 +530,9 @@ int opt2s_mx4_project_row(const void *x, int64_t cols, int32_t x_dtype, const op
                           int32_t dtype, cudaStream_t stream);
 
 /* CTAs of the products that gave up a bounded wait on the current device
- * since the library was loaded (0 unless the hardware or the library is at
- * fault; their outputs are then not written).  Waits for the device. */
+ * since the library was loaded: 0 unless the hardware or the library is at
+ * fault.  The outputs of a call with such a CTA are undefined.  Waits for all
+ * streams of the device, so it may not be called while one is captured. */
 int opt2s_mx4_errors(uint32_t *count);
 
 /*

@@ -12,8 +12,9 @@
  *
  * The host-only queries below are exported by the library.  The forcing
  * knobs (opt2s_testing_set_chunk_elems, opt2s_testing_set_launch), the fault
- * injection (opt2s_testing_fail_allocs) and the division check
- * (opt2s_testing_check_division) exist only in the test build of the
+ * injection (opt2s_testing_fail_allocs), the division check
+ * (opt2s_testing_check_division) and the check of waits that give up
+ * (opt2s_testing_wait_runs_out) exist only in the test build of the
  * library, libopt2s_testing.so (the same kernels, compiled once and linked
  * into both); the product libopt2s.so does not export them, and its launch
  * geometry cannot be changed.
@@ -105,6 +106,13 @@ int opt2s_testing_unorm_tables(const TensorListDesc *desc, int32_t algo, int64_t
  * results differ (NaN equals NaN) to *mismatches.  Synchronous; allocates a
  * counter on the device. */
 int opt2s_testing_check_division(uint64_t seed, int64_t n, int32_t mode, int64_t *mismatches);
+
+/* Test build only.  `ctas` CTAs of `threads` threads (<= 1,024) that each wait
+ * for a barrier that nothing completes, at most `limit` (<= 65,536) attempts,
+ * as the 4-bit products wait for their copies.  counts[0]: what they added to
+ * the error count (opt2s_mx4_errors counts CTAs); counts[1]: threads that
+ * gave up.  Synchronous; allocates the counters on the device. */
+int opt2s_testing_wait_runs_out(int32_t ctas, int32_t threads, uint32_t limit, uint32_t *counts);
 
 /* Test build only.  Fault injection on the host: the next `count` device
  * allocations of plan creation fail as if the device were out of memory

@@ -136,3 +136,11 @@ def test_the_error_count_waits_for_every_stream():
     assert not done.query()
     binding.check(binding.lib().opt2s_mx4_errors(ctypes.byref(n)), "opt2s_mx4_errors")
     assert done.query() and n.value == 0
+
+
+@pytest.mark.parametrize("ctas,threads", [(1, 1), (1, 32), (3, 384), (300, 96)])
+def test_a_wait_that_runs_out_counts_its_cta_once(testing_lib, ctas, threads):
+    """A wait has a limit: each thread returns, and the error count grows by
+    the CTAs that gave up, not by their threads."""
+    from elementwise_optimizer_b200 import binding
+    assert binding.testing_wait_runs_out(ctas, threads, 1000) == (ctas, ctas * threads)
