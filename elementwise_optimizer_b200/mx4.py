@@ -23,9 +23,13 @@ torch's current stream of it; nothing is kept between calls, and every call
 may be captured in a CUDA graph (a backward pass as torch allows it: while it
 is captured, no graph of the same leaves made outside may be alive).  Errors
 raise ``Opt2sError`` (the library's status) or ValueError/TypeError for
-arguments that do not fit together.
+arguments that do not fit together.  What only the device can know, a product
+that gave up waiting for its own copies, ``check_errors`` reports: it waits
+for the device, so the calls themselves do not ask.
 """
 from __future__ import annotations
+
+import ctypes
 
 import torch
 
@@ -118,6 +122,19 @@ def _fields(m):
     if not isinstance(m, MX4Tensor):
         raise TypeError("a product's operands are MX4Tensors")
     return m._fields
+
+
+def check_errors(device=None) -> None:
+    """Raises if a product on `device` (the current one) gave up waiting for
+    its own copies since the library was loaded: the hardware or the library
+    is then at fault, and that product's outputs are undefined.  Waits for all
+    streams of the device (not while one is captured)."""
+    count = ctypes.c_uint32()
+    with torch.cuda.device(device):
+        B.check(B.lib().opt2s_mx4_errors(ctypes.byref(count)), "opt2s_mx4_errors")
+    if count.value:
+        raise RuntimeError(f"{count.value} CTAs of 4-bit products gave up waiting for their copies; "
+                           "the outputs of those products are undefined")
 
 
 def empty_pair(x: torch.Tensor) -> tuple:

@@ -144,3 +144,10 @@ def test_a_wait_that_runs_out_counts_its_cta_once(testing_lib, ctas, threads):
     the CTAs that gave up, not by their threads."""
     from elementwise_optimizer_b200 import binding
     assert binding.testing_wait_runs_out(ctas, threads, 1000) == (ctas, ctas * threads)
+
+
+def test_check_errors(mx4):
+    w = mx4.quantize(normal((300, 8192), 71))
+    mx4.project(normal((17, 8192), 72), w)
+    mx4.check_errors()
+    mx4.check_errors(w.device)

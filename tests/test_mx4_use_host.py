@@ -62,3 +62,30 @@ def test_kept_copies_are_no_inference_tensors(monkeypatch):
         pair = opt.mx4_copies(own)
         assert torch.empty(1).is_inference()
     assert not any(t.is_inference() for t in pair) and opt.mx4_copies(own) is pair
+
+
+def test_check_errors(monkeypatch):
+    """The library's count of waits that gave up, as an exception."""
+    import contextlib
+
+    from elementwise_optimizer_b200 import binding as B, mx4
+    library, found, entered = B.lib(), 0, []
+
+    class Fake:
+        opt2s_error_string, opt2s_last_cuda_error = library.opt2s_error_string, library.opt2s_last_cuda_error
+
+        @staticmethod
+        def opt2s_mx4_errors(count):
+            count._obj.value = max(found, 0)
+            return min(found, 0)
+
+    monkeypatch.setattr(B, "lib", lambda: Fake)
+    monkeypatch.setattr(torch.cuda, "device", lambda d: entered.append(d) or contextlib.nullcontext())
+    assert mx4.check_errors() is None and mx4.check_errors("cuda:1") is None
+    assert entered == [None, "cuda:1"]
+    found = 3
+    with pytest.raises(RuntimeError, match="3 CTAs"):
+        mx4.check_errors()
+    found = -4
+    with pytest.raises(B.Opt2sError):
+        mx4.check_errors()
