@@ -370,15 +370,18 @@ Tensor linear(const Tensor& x, const Tensor& weight, const OptTensor& offsets, c
                       message("x ", x.sizes(), " does not fit the weight ", weight.sizes()));
     TORCH_CHECK_VALUE(x.is_cuda() && x.device() == weight.device(), "x and weight must be on one CUDA device");
     const int64_t n = weight.size(-2);
+    const bool grad = at::GradMode::is_enabled(), need_x = grad && x.requires_grad();
     TORCH_CHECK_VALUE(n >= 1, "a layer has at least one output");
     if (offsets)
         TORCH_CHECK_VALUE(check_offsets(*offsets, x.device()) == weight.size(0),
                           "offsets must hold one value more than there are experts");
     if (wq.codes.defined()) {
         const int64_t slabs = weight.dim() == 3 ? weight.size(0) : 1, k = weight.size(-1);
-        TORCH_CHECK_VALUE(wq.slabs == slabs && wq.rows == n && wq.cols == k && wt.slabs == slabs && wt.rows == k && wt.cols == n &&
-                              wq.codes.device() == x.device() && wt.codes.device() == x.device(),
+        const bool both = wt.codes.defined();
+        TORCH_CHECK_VALUE(wq.slabs == slabs && wq.rows == n && wq.cols == k && wq.codes.device() == x.device() &&
+                              (!both || (wt.slabs == slabs && wt.rows == k && wt.cols == n && wt.codes.device() == x.device())),
                           message("copies are not those of a weight ", weight.sizes()));
+        TORCH_CHECK_VALUE(both || !need_x, "x needs a gradient, which takes the weight's transposed copy too");
     }
     OptTensor bytes;
     if (noise) {
@@ -390,8 +393,7 @@ Tensor linear(const Tensor& x, const Tensor& weight, const OptTensor& offsets, c
     }
     dtype_code(x.scalar_type());
     dtype_code(weight.scalar_type());
-    const bool grad = at::GradMode::is_enabled();
-    return Linear::apply(x, weight, offsets, wq, wt, bytes, grad && x.requires_grad(), grad && weight.requires_grad());
+    return Linear::apply(x, weight, offsets, wq, wt, bytes, need_x, grad && weight.requires_grad());
 }
 
 using Fields = std::tuple<Tensor, Tensor, int64_t, int64_t, int64_t>;

@@ -210,14 +210,16 @@ def project_grouped(x: torch.Tensor, wq: MX4Tensor, offsets: torch.Tensor,
 
 
 def _copies(copies):
-    return (None, None) if copies is None else (_fields(copies[0]), _fields(copies[1]))
+    if copies is None:
+        return None, None
+    return _fields(copies[0]), None if copies[1] is None else _fields(copies[1])
 
 
 def linear(x: torch.Tensor, weight: torch.Tensor, copies: tuple | None = None,
            noise: torch.Tensor | None = None) -> torch.Tensor:
     """x [..., K] through weight [N, K] in 4 bits: [..., N] in x's dtype, with
     gradients in x's and weight's dtypes.  copies: the weight's pair, kept by
-    the caller; noise: random bytes (uint8, the output's shape) that round the
+    the caller (its second form may be None where x needs no gradient); noise: random bytes (uint8, the output's shape) that round the
     output's gradient stochastically."""
     return _extension().mx4_linear(x, weight, None, *_copies(copies), noise)
 

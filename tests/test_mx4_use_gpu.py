@@ -151,3 +151,26 @@ def test_check_errors(mx4):
     mx4.project(normal((17, 8192), 72), w)
     mx4.check_errors()
     mx4.check_errors(w.device)
+
+
+def test_layers_with_the_row_form_alone(mx4):
+    """A program that serves keeps one form of a weight.  The other is needed
+    for the input's gradient only."""
+    w, ws = normal((40, 96), 81), normal((3, 40, 96), 82)
+    x, off = normal((9, 96), 83), offsets_of([4, 0, 5])
+    q, qs = mx4.quantize(w), mx4.quantize(ws)
+    xg = x.clone().requires_grad_()
+    assert torch.equal(mx4.linear(x, w, copies=(q, None)), mx4.linear(x, w))
+    assert torch.equal(mx4.linear_grouped(x, ws, off, copies=(qs, None)), mx4.linear_grouped(x, ws, off))
+    with torch.no_grad():
+        assert torch.equal(mx4.linear(xg, w, copies=(q, None)), mx4.linear(x, w))
+    wg = w.clone().requires_grad_()           # the weight's own gradient takes no copy
+    dy = normal((9, 40), 84)
+    got, = torch.autograd.grad(mx4.linear(x, wg, copies=(q, None)), wg, dy)
+    assert torch.equal(got, torch.autograd.grad(mx4.linear(x, wg), wg, dy)[0])
+    for call in (lambda: mx4.linear(xg, w, copies=(q, None)), lambda: mx4.linear_grouped(xg, ws, off, copies=(qs, None)),
+                 lambda: mx4.linear(x, w, copies=(qs, None)), lambda: mx4.linear(x, w, copies=(mx4.quantize(w.t().contiguous()), None))):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(TypeError):
+        mx4.linear(x, w, copies=(None, mx4.quantize_pair(w)[1]))
