@@ -1010,9 +1010,8 @@ cudaError_t launch_as(Mx4GemmArgs a, const Mx4GemmOperands& op, int sms, cudaStr
     if (tiles > INT32_MAX / 8) return cudaErrorInvalidConfiguration;
     a.tiles = static_cast<int>(tiles);
     if (tiles == 0) return cudaSuccess;
-    constexpr int kResident = G::kTmemCols <= 256 && G::kSmem < 104000 ? 2 : 1;      // CTAs an SM holds
     const int cluster = PAIR ? 2 : a.split;
-    const int64_t ctas = a.split > 1 ? tiles * cluster : std::min<int64_t>(tiles, sms / cluster * kResident) * cluster;
+    const int64_t ctas = a.split > 1 ? tiles * cluster : std::min<int64_t>(tiles, sms / cluster) * cluster;
     auto* k = mx4_gemm_kernel<BN, SWAP, PAIR>;
     static std::atomic<uint64_t> allowed{0};
     if ((e = allow_shared(k, G::kSmem, allowed)) != cudaSuccess) return e;
