@@ -249,9 +249,9 @@ struct Geo {
     static constexpr int kSmem = kStages * (kStageCodes + kStageScales) + kOutBytes + 1024;
     static constexpr int kQCols = 4 * kQAtoms;                  // TMEM columns of one group's Q scales
     static constexpr int kSfCols = 8 + 2 * kQCols;
-    static constexpr int kSfSlots = BN == 256 ? 4 : kStages;
+    // A stage's scales have TMEM columns of their own, free again when the stage is.
     static constexpr int kSfBase = kAccStep + BN;
-    static constexpr int kUsedCols = kSfBase + kSfSlots * kSfCols;
+    static constexpr int kUsedCols = kSfBase + kStages * kSfCols;
     static constexpr int kTmemCols = kUsedCols <= 128 ? 128 : (kUsedCols <= 256 ? 256 : 512);
     static_assert(kUsedCols <= 512, "TMEM columns");
     static_assert(kSmem + 2 * 4 * (kMaxGroups + 1) + 512 <= 232448, "shared memory");
@@ -662,8 +662,7 @@ mx4_gemm_kernel(const __grid_constant__ Mx4GemmMaps maps, const Mx4GemmArgs a)
             // branch, a stage took 1,300 cycles to issue and 512 to compute.
             // kind::mxf4: E2M1 operands (1), E8M0 scales, M = 128 (pair: 256), N = BN
             constexpr uint32_t kIdesc = 1u << 7 | 1u << 10 | static_cast<uint32_t>(BN >> 3) << 17 | 1u << 23 | (PAIR ? 2u : 1u) << 27;
-            uint32_t n = 0, s = 0, ph = 0, slot = 0;
-            uint32_t es = 0, eph = 0, ahead = 0;         // the stage kSfSlots before, and how many stages were issued (up to kSfSlots)
+            uint32_t n = 0, s = 0, ph = 0;
             bool ok = true;
             for (int t = t0; t < tiles && ok; t += dt) {
                 const Tile o = tile_at<BN, SWAP, PAIR>(a, start, first, t, half);
@@ -679,18 +678,9 @@ mx4_gemm_kernel(const __grid_constant__ Mx4GemmMaps maps, const Mx4GemmArgs a)
                 const uint32_t d = tmem + b * G::kAccStep;
                 for (int k = 0; k < steps; k += 4) {
                     if (!(ok = warp_wait(ready(s), ph, &abort_flag))) break;
-                    if constexpr (G::kSfSlots < G::kStages) {
-                        // the slot's last readers: the MMAs of kSfSlots stages before
-                        if (ahead < G::kSfSlots) {
-                            ++ahead;
-                        } else {
-                            if (!(ok = warp_wait(empty(es), eph, &abort_flag))) break;
-                            if (++es == G::kStages) { es = 0; eph ^= 1; }
-                        }
-                    }
                     fence_after();
                     const uint32_t c = codes_at + s * G::kStageCodes, sf_from = sf_at + s * G::kStageScales;
-                    const uint32_t sf = tmem + G::kSfBase + slot * G::kSfCols;
+                    const uint32_t sf = tmem + G::kSfBase + s * G::kSfCols;
                     const uint64_t pd = tile_desc(c), qd = tile_desc(c + G::kCodesP);
                     if (elect_one()) {
 #pragma unroll
@@ -712,7 +702,6 @@ mx4_gemm_kernel(const __grid_constant__ Mx4GemmMaps maps, const Mx4GemmArgs a)
                     }
                     __syncwarp();
                     if (++s == G::kStages) { s = 0; ph ^= 1; }
-                    if (++slot == G::kSfSlots) slot = 0;
                 }
                 ++n;
             }
