@@ -174,3 +174,78 @@ def test_layers_with_the_row_form_alone(mx4):
             call()
     with pytest.raises(TypeError):
         mx4.linear(x, w, copies=(None, mx4.quantize_pair(w)[1]))
+
+
+def added(before, y, tol, dtype):
+    """(value, tolerance) of rounding before + s to `dtype`, s an fp32 sum
+    within `tol` of y: the addition rounds to fp32 (2^-24 of a result of at
+    most |before + y| + tol), and the result once more to `dtype`."""
+    want = before + y
+    tol = tol + 2.0 ** -24 * (want.abs() + tol)
+    if dtype != torch.float32:
+        tol = tol + torch.finfo(dtype).eps / 2 * (want.abs() + tol)
+    return want, tol
+
+
+def strided(shape, dtype, seed, wide):
+    """(a random view of `shape` whose rows are further apart, its storage)."""
+    store = normal((*shape[:-1], shape[-1] + wide), seed, dtype=dtype)
+    return store[..., :shape[-1]], store
+
+
+# the variants of the product: the swapped kernels (up to 16, 32 and 64 rows),
+# whole and with the contraction cut over a cluster, single CTAs and pairs
+@pytest.mark.parametrize("m,n,k", [(1, 40, 300), (16, 300, 8192), (17, 300, 8192), (30, 70, 200), (60, 131, 700), (50, 200, 8192),
+                                   (100, 260, 520), (4000, 4090, 96)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("wide", [0, 13, 16])
+def test_accumulate_in_every_variant(mx4, m, n, k, dtype, wide):
+    a, b = normal((m, k), 41, 0.25), normal((n, k), 42, 0.25)
+    out, store = strided((m, n), dtype, 43, wide)
+    before = store.clone()
+    mx4.matmul(mx4.quantize(a), mx4.quantize(b), out=out, accumulate=True)
+    y, tol = product_bound(round_ref(a), round_ref(b), torch.float32)
+    close(out, *added(before[..., :n].cpu().double(), y, tol, dtype))
+    assert torch.equal(store[..., n:], before[..., n:])
+
+
+@pytest.mark.parametrize("counts,extra", [([3, 0, 9, 1], 2), ([40, 0, 60], 0), ([300, 0, 129, 70], 5)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("wide", [0, 13])
+def test_accumulate_grouped(mx4, counts, extra, dtype, wide):
+    """Rows in no group stay as they were."""
+    rows, n, k = sum(counts) + extra, 140, 520
+    a, b = normal((rows, k), 51, 0.25), normal((len(counts), n, k), 52, 0.25)
+    out, store = strided((rows, n), dtype, 53, wide)
+    before = store.clone()
+    mx4.matmul_grouped(mx4.quantize(a), mx4.quantize(b), offsets_of(counts), out=out, accumulate=True)
+    av, bv, at = round_ref(a), round_ref(b), 0
+    for e, c in enumerate(counts):
+        s = slice(at, at + c)
+        at += c
+        y, tol = product_bound(av[s], bv[e], torch.float32)
+        close(out[s], *added(before[s, :n].cpu().double(), y, tol, dtype))
+    assert torch.equal(store[at:], before[at:]) and torch.equal(store[:, n:], before[:, n:])
+
+
+@pytest.mark.parametrize("n,k", [(40, 96), (531, 300), (2050, 2100)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("wide", [0, 13])
+def test_accumulate_expert_gradients(mx4, n, k, dtype, wide):
+    """A second batch's weight gradients added to the first's: an expert
+    without a token keeps what it has."""
+    counts = [70, 0, 130, 1]
+    dy, x, off = normal((201, n), 61, 0.25), normal((201, k), 62, 0.25), offsets_of(counts)
+    out, store = strided((4, n, k), dtype, 63, wide)
+    before = store.clone()
+    mx4.matmul_ragged(mx4.quantize_pair(dy, offsets=off)[1], mx4.quantize_pair(x, offsets=off)[1], off, out=out, accumulate=True)
+    at = 0
+    for e, c in enumerate(counts):
+        s = slice(at, at + c)
+        at += c
+        if not c:
+            assert torch.equal(store[e], before[e])
+            continue
+        y, tol = product_bound(turned_ref(dy[s]), turned_ref(x[s]), torch.float32)
+        close(out[e], *added(before[e, :, :k].cpu().double(), y, tol, dtype))
+    assert torch.equal(store[..., k:], before[..., k:])
