@@ -14,6 +14,9 @@ Q cuts its operand into blocks along the contraction, so every matrix of a
 training step is needed in two forms: ``quantize_pair`` makes both from one
 read.  Rounding to 4 bits is to nearest (even), or stochastic from random
 bytes that the caller gives; its gradient is taken as one (straight-through).
+Stochastic rounding keeps the mean of all but a block's largest elements:
+magnitudes between 6 and 8 times the block's scale 2^(floor(log2 amax) - 2)
+are cut to 6 either way, up to a quarter of them.
 ``copies`` skips the weight's quantisation: pass the pair that the optimizer
 keeps up to date (``optim.AdamW32bit(..., mx4=True)``, ``mx4_copies(w)``: its
 step writes them, see ``opt2s_step_mx4``), or one from ``quantize_pair``.

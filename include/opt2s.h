@@ -428,6 +428,9 @@ int opt2s_8bit_state_bits(int64_t numel, int64_t min_8bit_size);
  * Stochastic rounding takes its random numbers as an input, one byte r per
  * element: where x / 2^e (saturated) lies a fraction f of the way from one
  * code's magnitude to the next, the upper is taken when f > (r + 0.5) / 256.
+ * Over all bytes the mean is x up to 1/512 of the way between the codes, but
+ * not where x saturates: a magnitude between 6 and 8 times the scale, which
+ * only a block's largest elements have, becomes 6, up to a quarter less.
  *
  * opt2s_mx4 is `slabs` matrices of rows x cols, blocks along cols:
  *   codes   [slabs * rows][cols_p / 2] bytes, cols_p = cols rounded up to 128;

@@ -249,3 +249,23 @@ def test_accumulate_expert_gradients(mx4, n, k, dtype, wide):
         y, tol = product_bound(turned_ref(dy[s]), turned_ref(x[s]), torch.float32)
         close(out[e], *added(before[e, :, :k].cpu().double(), y, tol, dtype))
     assert torch.equal(store[..., k:], before[..., k:])
+
+
+def test_stochastic_rounding_is_biased_where_it_saturates(mx4):
+    """Over all 256 bytes the mean of a magnitude up to 6 times the scale is
+    the value, to half a byte's step of its spacing; between 6 and 8 times the
+    scale, where only a block's largest elements can lie, it is 6."""
+    values = [0.1, 0.7, 1.3, 2.9, 4.5, 5.99, 6.0, 6.3, 7.0, 7.99]
+    x = torch.zeros(256, 32)
+    x[:, 0] = 4.0                             # with the others the block's scale is 1
+    x[:, 1:1 + len(values)] = torch.tensor(values)
+    x[:, 16:16 + len(values)] = -torch.tensor(values)
+    r = torch.arange(256, dtype=torch.uint8)[:, None].expand(256, 32).contiguous()
+    mean = mx4.quantize(x.cuda(), noise=r.cuda()).dequantize().double().cpu().mean(0)
+    for i, value in enumerate(x[0, 1:1 + len(values)].double().tolist()):
+        step = 0.5 if value < 2 else 1.0 if value < 4 else 2.0
+        for got in (mean[1 + i].item(), -mean[16 + i].item()):
+            if value <= 6.0:
+                assert abs(got - value) <= step / 512 + 1e-12
+            else:
+                assert got == 6.0
