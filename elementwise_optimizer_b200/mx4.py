@@ -148,6 +148,8 @@ def empty_pair(x: torch.Tensor) -> tuple:
     rows, cols = x.shape[-2:]
     if slabs < 1 or rows < 1 or cols < 1:
         raise ValueError("a pair of 4-bit forms needs at least one element")
+    if not x.is_cuda:
+        raise ValueError("4-bit matrices are on CUDA devices")
     e = _extension()
     return (MX4Tensor._made(e.mx4_empty(slabs, rows, cols, x), x.dim() == 3),
             MX4Tensor._made(e.mx4_empty(slabs, cols, rows, x), x.dim() == 3))

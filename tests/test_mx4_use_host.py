@@ -89,3 +89,10 @@ def test_check_errors(monkeypatch):
     found = -4
     with pytest.raises(B.Opt2sError):
         mx4.check_errors()
+
+
+def test_no_storage_for_copies_outside_a_cuda_device():
+    """The step writes what empty_pair gives by its address."""
+    from elementwise_optimizer_b200 import mx4
+    with pytest.raises(ValueError, match="CUDA"):
+        mx4.empty_pair(torch.zeros(4, 8))
