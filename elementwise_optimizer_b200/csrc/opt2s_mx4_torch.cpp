@@ -454,6 +454,8 @@ void bind_mx4(py::module& m)
     m.def("mx4_product", [](const Fields& a, const Fields& b, const OptTensor& offsets, bool ragged,
                             std::optional<at::ScalarType> dtype, const OptTensor& out, bool accumulate) {
         TORCH_CHECK_VALUE(!out || !dtype || out->scalar_type() == *dtype, "out has another dtype than the one asked for");
+        TORCH_CHECK_VALUE(!out || !at::GradMode::is_enabled() || !out->requires_grad(),
+                          "out requires grad, and a product into a given tensor is not differentiated");
         at::NoGradGuard no_grad;
         const Matrix ma = matrix(a), mb = matrix(b);
         TORCH_CHECK_VALUE(ma.codes.device() == mb.codes.device(), "a product's operands must be on one device");

@@ -181,7 +181,8 @@ def quantize_pair(x: torch.Tensor, noise: torch.Tensor | None = None, offsets: t
 def matmul(a: MX4Tensor, b: MX4Tensor, dtype: torch.dtype | None = None, out: torch.Tensor | None = None,
            accumulate: bool = False) -> torch.Tensor:
     """a [M, K] times b [N, K] transposed: [M, N] in `dtype` (bf16), sums in
-    fp32.  out: where to write; accumulate: add to what it holds."""
+    fp32.  out: where to write (not differentiated); accumulate: add to what it
+    holds."""
     return _extension().mx4_product(_fields(a), _fields(b), None, False, dtype, out, accumulate)
 
 

@@ -269,3 +269,18 @@ def test_stochastic_rounding_is_biased_where_it_saturates(mx4):
                 assert abs(got - value) <= step / 512 + 1e-12
             else:
                 assert got == 6.0
+
+
+def test_no_product_into_a_tensor_of_a_graph(mx4):
+    """out= is not differentiated: written over, a tensor that requires grad
+    would keep the gradient of what it held before.  As torch's own out=."""
+    a, b = mx4.quantize(normal((9, 96), 91)), mx4.quantize(normal((40, 96), 92))
+    leaf = torch.zeros(9, 40, device="cuda", requires_grad=True)
+    for out in (leaf, leaf * 2):
+        for accumulate in (False, True):
+            version = out._version
+            with pytest.raises(ValueError, match="requires grad"):
+                mx4.matmul(a, b, out=out, accumulate=accumulate)
+            assert out._version == version
+    with torch.no_grad():
+        assert torch.equal(mx4.matmul(a, b, out=leaf), mx4.matmul(a, b, torch.float32))
