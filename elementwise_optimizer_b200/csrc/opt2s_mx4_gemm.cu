@@ -392,9 +392,9 @@ __device__ __forceinline__ void bulk_store(void* to, uint32_t from, uint32_t byt
 // D, whose rows start on 32 bytes: through NB buffers of 32 rows x 128 bytes.
 // With PART false all 32 rows exist and a buffer is stored by TMA in whole
 // lines (swizzled as the output's tensor map expects, whose bounds cut columns
-// behind D's last).  With PART true `rows` of them exist, and each of these is
-// a bulk copy of its lane's (D's columns then end on 16 bytes; the buffer's
-// rows are 144 bytes apart against bank conflicts).  chunk(i) is the first of
+// behind D's last, which end on 16 bytes).  With PART true `rows` of them
+// exist, and each of these is a bulk copy of its lane's (the buffer's rows are
+// 144 bytes apart against bank conflicts).  chunk(i) is the first of
 // the 32 columns that come i-th; release() is called once the first FIRST of
 // them (three, in registers together) or all (FIRST = 0) are read.  ZERO:
 // zeros instead.
@@ -460,8 +460,8 @@ __device__ __forceinline__ void store_tile(const CUtensorMap& map, const Mx4Gemm
     if constexpr (FIRST == 0 && !ZERO) release();
 }
 
-// The same where rows are missing (1 to 32 exist), D's rows do not start on 32
-// bytes, or D is added to: each row as 32 neighbouring elements of the warp
+// The same (1 to 32 rows exist) where D's rows do not start on 32 bytes or do
+// not end on 16, or D is added to: each row as 32 neighbouring elements of the warp
 // (stored by the lanes that hold the rows, 32 rows an instruction, 999 x 531 x
 // 1,000 into fp32 took 28 us; so, 8 us).  From zeros when ZERO.
 template <int DT, int BN, int FIRST, bool ZERO, typename Chunk, typename Release>
@@ -821,7 +821,7 @@ mx4_gemm_kernel(const __grid_constant__ Mx4GemmMaps maps, const Mx4GemmArgs a)
                             if (a.tma_store && rows >= 32)
                                 store_tile<DT, BN, kFirst, G::kOutBuffers, false, false>(maps.d, a, o, acc, warp, lane, 32, smem_u32(buf),
                                                                                   chunk, release);
-                            else if (a.tma_store && a.d_cols * (DT == kF32 ? 4 : 2) % 16 == 0)
+                            else if (a.tma_store)
                                 store_tile<DT, BN, kFirst, G::kOutBuffers, true, false>(maps.d, a, o, acc, warp, lane, rows, smem_u32(buf),
                                                                                  chunk, release);
                             else
@@ -987,7 +987,9 @@ cudaError_t launch_as(Mx4GemmArgs a, const Mx4GemmOperands& op, int sms, cudaStr
     if ((e = codes_map(enc, &maps.q_codes, q.codes, q.code_rows, q.pitch, G::kQRows)) != cudaSuccess) return e;
     if ((e = scales_map(enc, &maps.p_scales, p.scales, p.scale_rows, p.pitch / 64, G::kSfP)) != cudaSuccess) return e;
     if ((e = scales_map(enc, &maps.q_scales, q.scales, q.scale_rows, q.pitch / 64, G::kSfQ)) != cudaSuccess) return e;
-    a.tma_store = !SWAP && a.vec && !a.accumulate;
+    // A bulk store writes whole 16-byte pieces: where D's columns end inside
+    // one it would write into what stands behind them.
+    a.tma_store = !SWAP && a.vec && !a.accumulate && a.d_cols * elem_bytes(a.dtype) % 16 == 0;
     if (a.tma_store && (e = out_map(enc, &maps.d, a)) != cudaSuccess) return e;
     constexpr int kP = PAIR ? 2 * kPRows : kPRows, kX = SWAP ? BN : kP, kW = SWAP ? kPRows : BN;
     a.w_tiles = static_cast<int>((a.w_rows + kW - 1) / kW);

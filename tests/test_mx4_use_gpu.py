@@ -284,3 +284,41 @@ def test_no_product_into_a_tensor_of_a_graph(mx4):
             assert out._version == version
     with torch.no_grad():
         assert torch.equal(mx4.matmul(a, b, out=leaf), mx4.matmul(a, b, torch.float32))
+
+
+# (rows, columns, contraction): single CTAs' tiles and pairs', whole ones and partial ones
+@pytest.mark.parametrize("m,n,k", [(128, 5, 64), (1217, 5, 33), (384, 132, 96), (384, 133, 200), (400, 136, 96), (4096, 4093, 64)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+def test_columns_beside_an_output_stay(mx4, m, n, k, dtype):
+    """Rows that start on 32 bytes and end off 16: what stands between them
+    belongs to the caller, and there may be nothing behind the last."""
+    a, b = normal((m, k), 101, 0.25), normal((n, k), 102, 0.25)
+    ldd = (n + 15) // 16 * 16
+    store = normal((m * ldd + 64,), 103, dtype=dtype)
+    before, rows = store.clone(), store[:m * ldd].view(m, ldd)
+    mx4.matmul(mx4.quantize(a), mx4.quantize(b), out=rows[:, :n])
+    close(rows[:, :n], *product_bound(round_ref(a), round_ref(b), dtype))
+    assert torch.equal(rows[:, n:], before[:m * ldd].view(m, ldd)[:, n:])
+    assert torch.equal(store[m * ldd:], before[m * ldd:])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_columns_beside_grouped_outputs_stay(mx4, dtype):
+    """The same for groups, and for the zeros of an expert without a token."""
+    counts, n, k = [256, 0, 384], 133, 77
+    rows, off = sum(counts), offsets_of(counts)
+    x, w, dy = normal((rows, k), 111, 0.25), normal((3, n, k), 112, 0.25), normal((rows, n), 113, 0.25)
+    y, dw = normal((rows, 144), 114, dtype=dtype), normal((3, n, 80), 115, dtype=dtype)
+    y0, dw0 = y.clone(), dw.clone()
+    mx4.matmul_grouped(mx4.quantize(x), mx4.quantize(w), off, out=y[:, :n])
+    mx4.matmul_ragged(mx4.quantize_pair(dy, offsets=off)[1], mx4.quantize_pair(x, offsets=off)[1], off, out=dw[..., :k])
+    assert torch.equal(y[:, n:], y0[:, n:]) and torch.equal(dw[..., k:], dw0[..., k:])
+    at = 0
+    for e, c in enumerate(counts):
+        s = slice(at, at + c)
+        at += c
+        if not c:
+            assert not dw[e, :, :k].any()
+            continue
+        close(y[s, :n], *product_bound(round_ref(x[s]), round_ref(w[e]), dtype))
+        close(dw[e, :, :k], *product_bound(turned_ref(dy[s]), turned_ref(x[s]), dtype))
