@@ -322,3 +322,34 @@ def test_columns_beside_grouped_outputs_stay(mx4, dtype):
             continue
         close(y[s, :n], *product_bound(round_ref(x[s]), round_ref(w[e]), dtype))
         close(dw[e, :, :k], *product_bound(turned_ref(dy[s]), turned_ref(x[s]), dtype))
+
+
+@pytest.mark.parametrize("counts,lead,behind", [([70, 0, 130], 3, 5), ([3, 0, 9, 1], 1, 2), ([300, 129], 40, 1)])
+@pytest.mark.parametrize("noise", [False, True])
+def test_rows_in_no_group_reach_nothing(mx4, counts, lead, behind, noise):
+    """NaN and infinities in padding rows before and behind the groups: their
+    outputs and gradients are zero, everything else as without them; and a NaN
+    in one expert's token stays with that expert."""
+    rows, n, k, tokens = lead + sum(counts) + behind, 140, 96, slice(lead, lead + sum(counts))
+    x, dy, w = normal((rows, k), 121), normal((rows, n), 122), normal((len(counts), n, k), 123).requires_grad_()
+    r = torch.randint(0, 256, (rows, n), dtype=torch.uint8).cuda() if noise else None
+    off = offsets_of(counts) + lead
+
+    def run(x, dy):
+        x = x.clone().requires_grad_()
+        y = mx4.linear_grouped(x, w, off, noise=r)
+        return (y.detach(), *torch.autograd.grad(y, (x, w), dy))
+
+    want = run(x, dy)
+    for t in (x, dy):
+        t[:lead], t[tokens.stop:] = float("nan"), float("inf")
+    got = run(x, dy)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b) and a.isfinite().all()
+    for a in got[:2]:
+        assert not a[:lead].any() and not a[tokens.stop:].any()
+    x[lead, 5] = dy[lead, 7] = float("nan")          # the first expert's first token
+    y, dx, dw = run(x, dy)
+    for a in (y, dx):
+        assert a[lead].isnan().all() and torch.equal(a[lead + 1:], want[0 if a is y else 1][lead + 1:])
+    assert dw[0].isnan().any() and torch.equal(dw[1:], want[2][1:])
