@@ -24,9 +24,12 @@
 // the clock.  The contraction's loads arrive about 1,000 cycles before they are
 // needed.
 //
-// Every wait is bounded: a wait that runs out raises the CTA's abort flag and
-// the library's error flag (opt2s_mx4_errors), and the CTA drains its copies,
-// frees its TMEM and returns.
+// Every wait on a shared-memory barrier is bounded: one that runs out raises
+// the CTA's abort flag and adds to the library's count (opt2s_mx4_errors), and
+// the CTA drains its copies, frees its TMEM and returns.  The other waits have
+// no limit and need none: every thread of a cluster reaches its barriers,
+// since all loops before them end, and TMEM is free at once, since shared
+// memory lets no more of these CTAs share an SM than two of 128 columns.
 #include <type_traits>
 
 #include <cuda.h>

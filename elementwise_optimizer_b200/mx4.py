@@ -224,9 +224,12 @@ def _copies(copies):
 def linear(x: torch.Tensor, weight: torch.Tensor, copies: tuple | None = None,
            noise: torch.Tensor | None = None) -> torch.Tensor:
     """x [..., K] through weight [N, K] in 4 bits: [..., N] in x's dtype, with
-    gradients in x's and weight's dtypes.  copies: the weight's pair, kept by
-    the caller (its second form may be None where x needs no gradient); noise: random bytes (uint8, the output's shape) that round the
-    output's gradient stochastically."""
+    gradients in x's and weight's dtypes.  x and the output's gradient may have
+    any strides (where rows are not contiguous they are copied); the weight,
+    which is read in place, has contiguous rows: a transposed view is refused.
+    copies: the weight's pair, kept by the caller (its second form may be None
+    where x needs no gradient); noise: random bytes (uint8, the output's shape)
+    that round the output's gradient stochastically."""
     return _extension().mx4_linear(x, weight, None, *_copies(copies), noise)
 
 
