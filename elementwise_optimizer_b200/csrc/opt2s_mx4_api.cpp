@@ -34,6 +34,9 @@ Range span(const void* p, int64_t bytes, bool written)
     return {lo, lo + static_cast<uintptr_t>(bytes), written};
 }
 
+// Whether n things `stride` elements apart span more than any address space.
+bool too_far(int64_t n, int64_t stride) { return n > 1 && stride > (int64_t{1} << 54) / (n - 1); }
+
 bool aligned(const void* p, uintptr_t k) { return reinterpret_cast<uintptr_t>(p) % k == 0; }
 
 // Checks a matrix and appends its two ranges (none when it has no rows).
@@ -70,7 +73,7 @@ int product(const opt2s_mx4* a, const opt2s_mx4* b, const int32_t* offsets, int3
     if (!good_dtype(dtype) || (accumulate != 0 && accumulate != 1) || (fill_rest != 0 && fill_rest != 1))
         return OPT2S_ERR_INVALID_ARG;
     if (a->cols != b->cols || a->slabs != 1 || (accumulate && fill_rest)) return OPT2S_ERR_INVALID_ARG;
-    if (ldd < b->rows || ldd > (int64_t{1} << 40)) return OPT2S_ERR_INVALID_ARG;
+    if (ldd < b->rows || ldd > (int64_t{1} << 40) || too_far(d_rows, ldd)) return OPT2S_ERR_INVALID_ARG;
     if (d_rows == 0 || b->rows == 0) return OPT2S_OK;
     const int es = opt2s::elem_bytes(dtype);
     if (!d || !aligned(d, es)) return OPT2S_ERR_INVALID_ARG;
@@ -121,6 +124,7 @@ OPT2S_API int opt2s_mx4_quantize(const opt2s_mx4_source* src, const opt2s_mx4* q
     if (!good_sizes(src->slabs, src->rows, src->cols) || src->row_stride < 0 || src->slab_stride < 0)
         return OPT2S_ERR_INVALID_ARG;
     if (src->row_stride > (int64_t{1} << 40) || src->slab_stride > (int64_t{1} << 40)) return OPT2S_ERR_INVALID_ARG;
+    if (too_far(src->rows, src->row_stride) || too_far(src->slabs, src->slab_stride)) return OPT2S_ERR_INVALID_ARG;
     if (!offsets && groups != 0) return OPT2S_ERR_INVALID_ARG;
     if (offsets && (good_groups(offsets, groups) != OPT2S_OK || src->slabs != 1)) return OPT2S_ERR_INVALID_ARG;
     Range r[7];

@@ -96,3 +96,23 @@ def test_no_storage_for_copies_outside_a_cuda_device():
     from elementwise_optimizer_b200 import mx4
     with pytest.raises(ValueError, match="CUDA"):
         mx4.empty_pair(torch.zeros(4, 8))
+
+
+def test_no_stride_leaves_the_address_space():
+    """Rows or slabs so far apart that their span overflows are refused, not
+    compared with the other operands as whatever is left of it."""
+    import ctypes
+
+    from elementwise_optimizer_b200 import binding as B
+    L, base = B.lib(), 1 << 40
+    rows, far = 1 << 22, 1 << 40
+
+    def matrix(slabs, rows, cols, at):
+        return B.opt2s_mx4(base + at, base + at + (1 << 36), slabs, rows, cols)
+
+    for slabs, n, row_stride, slab_stride in ((1, rows, far, 0), (60000, 4, 8, far)):
+        s = B.opt2s_mx4_source(base, None, slabs, n, 8, row_stride, slab_stride, B.OPT2S_F32, 0)
+        q = matrix(slabs, n, 8, 1 << 38)
+        assert L.opt2s_mx4_quantize(ctypes.byref(s), ctypes.byref(q), None, None, 0, None) == -1
+    a, b = matrix(1, rows, 256, 1 << 38), matrix(1, 10, 256, 1 << 39)
+    assert L.opt2s_mx4_matmul(ctypes.byref(a), ctypes.byref(b), base, far, B.OPT2S_F32, 0, None) == -1
